@@ -76,6 +76,9 @@ extern "C" {
 #define SMLA_PAGE_BYTES 149504
 #define SMLA_MAX_TOPK 65536
 #define SMLA_WORKSPACE_HEADER 256
+#define SMLA_SPAN_TOKENS 64      /* a span: 64 consecutive tokens, a quarter of a page */
+#define SMLA_MAX_NSEL 1024       /* spans listed per request (65536 tokens, as SMLA_MAX_TOPK) */
+#define SMLA_MAX_SPANS (1 << 25) /* spans of a request */
 
 /* Tuning and test options for smla_decode_ex.  Zero-initialise for defaults. */
 typedef struct smla_options {
@@ -227,6 +230,62 @@ int smla_decode_noalloc(const void *q, const uint8_t *kv_cache, const int32_t *b
 int smla_write_kv(const void *latents, int latents_bf16, int n, const int32_t *req, const int32_t *pos,
                   const int32_t *block_table, int B, int max_blocks, int num_pages, uint8_t *kv_cache,
                   uint32_t *err, void *stream);
+
+/*
+ * smla_read_kv -- cached tokens read back (the inverse of smla_write_kv): token i, at
+ * position pos[i] of request req[i], as a dense 512-d latent: nope value =
+ * e4m3 * 2^(scale-127) (a 0xFF scale byte gives NaN), rope value as stored.  For a prompt
+ * chunk that attends to its cached prefix, or for moving tokens between caches.
+ *   out         device, [n][512], fp32 (out_bf16 = 0: exact) or bf16 (out_bf16 = 1: that
+ *               value rounded to nearest even; exact for scale bytes 10 and up within the
+ *               bf16 range), 16-byte aligned
+ *   err         device uint32 or NULL: SMLA_FLAG_BAD_PAGE is or-ed in when a token is out
+ *               of range (as in smla_write_kv); its row of out is zeros
+ *   The other arguments are those of smla_write_kv.  n >= 0 (0: nothing is launched).
+ */
+int smla_read_kv(const uint8_t *kv_cache, const int32_t *req, const int32_t *pos, int n, const int32_t *block_table,
+                 int B, int max_blocks, int num_pages, void *out, int out_bf16, uint32_t *err, void *stream);
+
+/*
+ * Spans: selection of what a request attends to, by 64-token spans.  Span j of request b is
+ * its tokens [64 j, min(64 j + 64, seq_lens[b])), which lie in page block_table[b][j / 4];
+ * there are ceil(seq_lens[b] / 64) of them.  A decode step that attends to a selection:
+ *   smla_write_kv      the new tokens
+ *   smla_span_keys     the spans they fell into: new keys
+ *   smla_span_scores   how much of the query's attention each span should get
+ *   smla_select_spans  the best spans, and their tokens as smla_decode's topk_idx
+ *   smla_decode_spans  (or smla_decode)  attention over them
+ */
+
+/*
+ * smla_span_keys -- recomputes the keys of n spans: the mean of the span's dequantised
+ * latents (the tokens below seq_lens[b]), summed in fp32, rounded to bf16.
+ *   req, span   device, int32 [n]: request and span of each key
+ *   keys        device, bf16 [num_pages][4][512], 16-byte aligned: key of span j of
+ *               request b at [block_table[b][j / 4]][j % 4] (written; the others are left)
+ *   err         device uint32 or NULL: SMLA_FLAG_BAD_PAGE is or-ed in when a span is skipped
+ *               (req outside [0, B), a span that holds no token of the request or lies behind
+ *               max_blocks, a page outside [0, num_pages)); nothing is written for it
+ *   n >= 0 (0: nothing is launched).  A span may be listed twice.  One launch on `stream`.
+ */
+int smla_span_keys(const uint8_t *kv_cache, const int32_t *block_table, const int32_t *seq_lens, const int32_t *req,
+                   const int32_t *span, int n, int B, int max_blocks, int num_pages, void *keys, uint32_t *err,
+                   void *stream);
+
+/*
+ * smla_select_spans -- per request the nsel spans with the highest scores, among them always
+ * its first keep_first and its last keep_last spans (0 <= keep_first + keep_last <= nsel).
+ * Ties go to the lower span; NaN scores rank with -inf, below every number.
+ *   scores      device, fp32 [B][width] (what smla_span_scores writes, or others of that
+ *               layout); spans at or behind `width` do not exist here
+ *   spans       device, int32 [B][nsel] (written): ascending, then -1 where the request has
+ *               fewer than nsel spans
+ *   topk_idx    device, int32 [B][64 nsel] or NULL (written): entry 64 i + t is token
+ *               64 spans[i] + t, or -1 if that is not below seq_lens[b]: smla_decode's topk_idx
+ *   1 <= nsel <= SMLA_MAX_NSEL, 1 <= width <= SMLA_MAX_SPANS, B >= 1.  One launch.
+ */
+int smla_select_spans(const float *scores, int width, const int32_t *seq_lens, int nsel, int keep_first,
+                      int keep_last, int32_t *spans, int32_t *topk_idx, int B, void *stream);
 
 /* Build identification string (static storage). */
 const char *smla_version(void);

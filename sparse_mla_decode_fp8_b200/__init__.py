@@ -19,6 +19,9 @@ from .binding import (  # noqa: F401
     library,
     num_splits,
     read_error,
+    read_kv,
+    select_spans,
+    span_keys,
     version,
     workspace_bytes,
     write_kv,

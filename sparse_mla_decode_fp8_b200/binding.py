@@ -3,7 +3,8 @@
 Names follow the C ABI (``include/smla.h``): ``decode`` -> ``smla_decode_ex``,
 ``combine`` -> ``smla_combine``, ``debug_gather`` -> ``smla_debug_gather``,
 ``workspace_bytes`` -> ``smla_workspace_bytes_ex``, ``read_error`` ->
-``smla_read_error``.  Tensors must already be on the current CUDA device, dense
+``smla_read_error``, and ``read_kv``, ``span_keys``, ``span_scores``,
+``select_spans``, ``decode_spans`` -> the entry points of the same names.  Tensors must already be on the current CUDA device, dense
 and of the documented dtype; nothing is copied or converted here.
 """
 from __future__ import annotations
@@ -23,6 +24,8 @@ SMLA_DEBUG_SKIP_FIRST_COMMIT = 0x1
 HEADS = 64
 DIM = 512
 PAGE_BYTES = 149504
+SPAN_TOKENS = 64
+PAGE_SPANS = 4
 
 _ERRORS = {-1: "invalid argument", -2: "unsupported device (needs sm_100)", -3: "CUDA runtime error",
            -4: "kernel launch failed"}
@@ -69,6 +72,12 @@ def library():
             lib.smla_debug_gather.restype = I
             lib.smla_write_kv.argtypes = [P, I, I, P, P, P, I, I, I, P, P, P]
             lib.smla_write_kv.restype = I
+            lib.smla_read_kv.argtypes = [P, P, P, I, P, I, I, I, P, I, P, P]
+            lib.smla_read_kv.restype = I
+            lib.smla_span_keys.argtypes = [P, P, P, P, P, I, I, I, I, P, P, P]
+            lib.smla_span_keys.restype = I
+            lib.smla_select_spans.argtypes = [P, I, P, I, I, I, P, P, I, P]
+            lib.smla_select_spans.restype = I
             lib.smla_version.restype = ctypes.c_char_p
             _lib = lib
     return _lib
@@ -207,3 +216,108 @@ def write_kv(latents, req, pos, block_table, kv_cache, err=None, stream=None) ->
         block_table.shape[0], block_table.shape[1], kv_cache.shape[0], _dev(kv_cache, torch.uint8, "kv_cache"), ep,
         _stream(stream))
     _check(rc, "smla_write_kv")
+
+
+# ---------------------------------------------------------------- long contexts: spans and reading back
+def _args(device, *tensors):
+    """Device pointers of (tensor, dtype, shape, name) entries, which must be dense CUDA
+    tensors of that dtype and shape (None entries of a shape are free) on ``device``, the
+    current one: the library launches on the current device."""
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise SmlaError(f"tensors must be on the current CUDA device, got {device}")
+    ptrs = []
+    for t, dtype, shape, name in tensors:
+        if t is None:
+            ptrs.append(None)
+            continue
+        p = _dev(t, dtype, name)
+        if t.device != device:
+            raise SmlaError(f"{name} is on {t.device}, others on {device}")
+        if shape is not None and (t.dim() != len(shape) or any(a is not None and a != b for a, b in zip(shape, t.shape))):
+            raise SmlaError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+        ptrs.append(p)
+    return ptrs
+
+
+def _device(t, name) -> torch.device:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise SmlaError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _new(stream, shape, dtype, device, zero=False) -> torch.Tensor:
+    """A tensor allocated on the stream that will write it."""
+    make = torch.zeros if zero else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream), device=device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=device)
+
+
+def _err(err, device):
+    if err is None:
+        return None
+    if not isinstance(err, torch.Tensor) or err.dtype not in (torch.int32, torch.uint32) or err.numel() < 1:
+        raise SmlaError("err must be a CUDA int32/uint32 tensor")
+    return _args(device, (err, err.dtype, None, "err"))[0]
+
+
+def read_kv(kv_cache, req, pos, block_table, out=None, out_dtype=None, err=None, stream=None):
+    """smla_read_kv: the cached tokens at position pos[i] of request req[i] as latents [n,512],
+    bf16 (the default) or fp32; rows of tokens out of range are zeros, and ``err`` receives
+    SMLA_FLAG_BAD_PAGE."""
+    dev = _device(kv_cache, "kv_cache")
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else torch.bfloat16
+    if out_dtype not in (torch.float32, torch.bfloat16):
+        raise SmlaError("out must be float32 or bfloat16")
+    n = req.shape[0] if isinstance(req, torch.Tensor) and req.dim() == 1 else -1
+    if out is None and n >= 0:
+        out = _new(stream, (n, DIM), out_dtype, dev)
+    c, r, p, t, o = _args(dev, (kv_cache, torch.uint8, (None, PAGE_BYTES), "kv_cache"), (req, torch.int32, (None,), "req"),
+                          (pos, torch.int32, (n,), "pos"), (block_table, torch.int32, (None, None), "block_table"),
+                          (out, out_dtype, (n, DIM), "out"))
+    rc = library().smla_read_kv(c, r, p, n, t, block_table.shape[0], block_table.shape[1], kv_cache.shape[0], o,
+                                1 if out_dtype == torch.bfloat16 else 0, _err(err, dev), _stream(stream))
+    _check(rc, "smla_read_kv")
+    return out
+
+
+def span_keys(kv_cache, block_table, seq_lens, req, span, keys, err=None, stream=None):
+    """smla_span_keys: recomputes the keys of span[i] of request req[i] in ``keys``
+    (bf16 [num_pages,4,512], returned); ``err`` receives SMLA_FLAG_BAD_PAGE when a span is
+    skipped."""
+    dev = _device(kv_cache, "kv_cache")
+    pages = kv_cache.shape[0]
+    n = req.shape[0] if isinstance(req, torch.Tensor) and req.dim() == 1 else -1
+    B, blocks = block_table.shape if isinstance(block_table, torch.Tensor) and block_table.dim() == 2 else (-1, -1)
+    c, t, l, r, s, k = _args(dev, (kv_cache, torch.uint8, (None, PAGE_BYTES), "kv_cache"),
+                             (block_table, torch.int32, (None, None), "block_table"),
+                             (seq_lens, torch.int32, (B,), "seq_lens"), (req, torch.int32, (None,), "req"),
+                             (span, torch.int32, (n,), "span"), (keys, torch.bfloat16, (pages, PAGE_SPANS, DIM), "keys"))
+    rc = library().smla_span_keys(c, t, l, r, s, n, B, blocks, pages, k, _err(err, dev), _stream(stream))
+    _check(rc, "smla_span_keys")
+    return keys
+
+
+def select_spans(scores, seq_lens, nsel: int, keep_first: int = 0, keep_last: int = 0, spans=None, topk_idx=None,
+                 tokens: bool = True, stream=None):
+    """smla_select_spans: (spans int32 [B,nsel], topk_idx int32 [B,64 nsel]), the second None
+    when ``tokens`` is false."""
+    dev = _device(scores, "scores")
+    B, width = scores.shape if scores.dim() == 2 else (-1, -1)
+    nsel, keep_first, keep_last = int(nsel), int(keep_first), int(keep_last)
+    if not 1 <= nsel <= 1024:
+        raise SmlaError("nsel must lie in [1, 1024]")
+    if spans is None:
+        spans = _new(stream, (max(B, 0), nsel), torch.int32, dev)
+    if topk_idx is None and tokens:
+        topk_idx = _new(stream, (max(B, 0), nsel * SPAN_TOKENS), torch.int32, dev)
+    x, l, s, i = _args(dev, (scores, torch.float32, (None, None), "scores"), (seq_lens, torch.int32, (B,), "seq_lens"),
+                       (spans, torch.int32, (B, nsel), "spans"),
+                       (topk_idx, torch.int32, (B, nsel * SPAN_TOKENS), "topk_idx"))
+    rc = library().smla_select_spans(x, width, l, nsel, keep_first, keep_last, s, i, B, _stream(stream))
+    _check(rc, "smla_select_spans")
+    return spans, topk_idx

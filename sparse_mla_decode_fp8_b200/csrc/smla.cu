@@ -36,7 +36,6 @@
 //     splits, or a bf16 output, write fp32 partials that combine_kernel merges.
 #include <cuda.h>
 #include <cuda_bf16.h>
-#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -47,10 +46,11 @@
 #include "../../include/smla.h"
 #include "sm100_ptx.cuh"
 #include "smla_device.cuh"
+#include "smla_host.cuh"
+#include "smla_tile.cuh"
 
 namespace smla {
 
-constexpr int kTile = 128;                     // topk slots per MMA tile (the M of S^T)
 constexpr int kWorkerWarps = 16;               // gather, dequantisation, softmax, epilogue
 constexpr int kWorkers = 32 * kWorkerWarps;    // 512
 constexpr int kCtlWarp = kWorkerWarps;         // warp 16: tensor memory, mbarriers, TMA, MMA issue
@@ -106,8 +106,6 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO2 = 256;
 constexpr uint32_t kTmemS = 384;
 constexpr uint32_t kTmemL = 448;
-constexpr uint32_t kIdescQK = idesc_bf16(128, 64, false, false);
-constexpr uint32_t kIdescPV = idesc_bf16(128, 64, true, true);
 constexpr uint32_t kIdescPV2 = idesc_bf16(128, 128, true, true);
 // log2 units: the running max m of a head is raised (and O^T, the sums rescaled) only when a
 // score exceeds it by more than this, so p = 2^(s - m) stays below 2^64.  P_hi + P_lo keep
@@ -157,43 +155,6 @@ struct DecodeParams {
 //   kEpiBf16  bf16 O (round to nearest even) and fp32 LSE, one split
 //   kEpiPair  two splits in a CTA pair (cluster) adding into the fp32 output
 enum Epilogue : int { kEpiF32 = 0, kEpiBf16 = 1, kEpiPair = 2 };
-
-// Reduces N (16 or 32) per-thread values across the 32 lanes of a warp, value i with
-// value i of every other lane.  Each round halves the live entries: a lane keeps the
-// half selected by its lane bit and sends the other half to its partner.  With N = 32
-// lane j ends with entry j; with N = 16 lanes 2j and 2j+1 end with entry j.
-template <bool kMax, int N>
-__device__ __forceinline__ float warp_transpose_reduce(float (&v)[N], int lane) {
-    static_assert(N == 16 || N == 32, "16 or 32 entries");
-#pragma unroll
-    for (int w = N / 2, off = 16; w >= 1; w >>= 1, off >>= 1) {
-        const bool upper = (lane & off) != 0;
-#pragma unroll
-        for (int i = 0; i < w; ++i) {
-            const float send = upper ? v[i] : v[i + w];
-            const float keep = upper ? v[i + w] : v[i];
-            const float got = __shfl_xor_sync(0xffffffffu, send, off);
-            v[i] = kMax ? fmaxf(keep, got) : keep + got;
-        }
-    }
-    if constexpr (N == 16) {
-        const float got = __shfl_xor_sync(0xffffffffu, v[0], 1);
-        return kMax ? fmaxf(v[0], got) : v[0] + got;
-    }
-    return v[0];
-}
-
-// 16 consecutive floats of shared memory (16-byte aligned) into registers.
-__device__ __forceinline__ void load16(const float *src, float (&v)[16]) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float4 t = reinterpret_cast<const float4 *>(src)[j];
-        v[4 * j] = t.x;
-        v[4 * j + 1] = t.y;
-        v[4 * j + 2] = t.z;
-        v[4 * j + 3] = t.w;
-    }
-}
 
 // Bounded wait on an mbarrier phase.  Gives up when another thread has aborted the
 // CTA or when `timeout_ns` passes (then it aborts the CTA and flags the error).
@@ -425,29 +386,6 @@ __device__ __forceinline__ bool dequant_tile(int i, int t, int lane, const Decod
 // all of them, so instructions between two MMAs directly slow the tensor core.  Every
 // wait is bounded; a failed wait stops the issue.
 //
-// Descriptor words (128-byte swizzle, see sw128_desc): the high word holds SBO = 1024
-// (8 rows of 128 bytes), the version and the swizzle mode; the low word holds the
-// address (16-byte units) and LBO.
-constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
-__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
-    return ((saddr >> 4) & 0x3FFFu) | (((lbo >> 4) & 0x3FFFu) << 16);
-}
-
-// S^T += K.Q^T over dims chunk cp: 2 K-blocks x 4 steps of K = 16 (the K rows are
-// 128 bytes per K-block, K-blocks 16 KB apart; Q K-blocks 8 KB apart).
-__device__ __forceinline__ void issue_qk_chunk(uint32_t d, uint32_t a_lo, uint32_t b_lo, bool first) {
-    if (first)
-        mma_bf16_ss(d, desc_from(a_lo, kDescHi), desc_from(b_lo, kDescHi), kIdescQK, 0u);
-    else
-        mma_bf16_ss_acc(d, desc_from(a_lo, kDescHi), desc_from(b_lo, kDescHi), kIdescQK);
-#pragma unroll
-    for (int k = 1; k < 8; ++k) {
-        const uint32_t ao = (k >> 2) * ((kTile * 128) >> 4) + (k & 3) * 2;
-        const uint32_t bo = (k >> 2) * (8192 >> 4) + (k & 3) * 2;
-        mma_bf16_ss_acc(d, desc_from(a_lo + ao, kDescHi), desc_from(b_lo + bo, kDescHi), kIdescQK);
-    }
-}
-
 // O^T chunk += V^T.P_hi^T + V^T.P_lo^T over the tile's 128 tokens: 8 steps of 16 tokens
 // (2 KB apart in the MN-major V^T and P^T), two N = 64 MMAs per step.
 __device__ __forceinline__ void issue_pv_chunk(uint32_t d, uint32_t a_lo, uint32_t bh_lo, uint32_t bl_lo,
@@ -1111,7 +1049,10 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const uint8_t *c
 // ======================================================================== host
 namespace {
 
-constexpr int kMaxDevices = 64;
+using smla::host::aligned;
+using smla::host::encode_q_map;
+using smla::host::kMaxDevices;
+using smla::host::round256;
 
 struct DeviceInfo {
     bool ready = false;
@@ -1121,39 +1062,6 @@ struct DeviceInfo {
 
 std::mutex g_mutex;
 DeviceInfo g_devices[kMaxDevices];
-PFN_cuTensorMapEncodeTiled_v12000 g_encode_tiled = nullptr;
-
-// cuTensorMapEncodeTiled from the driver, looked up once through the runtime.
-int tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000 &fn) {
-    std::lock_guard<std::mutex> lock(g_mutex);
-    if (g_encode_tiled == nullptr) {
-        void *f = nullptr;
-        cudaDriverEntryPointQueryResult q{};
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess || f == nullptr)
-            return SMLA_ERR_CUDA;
-        g_encode_tiled = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    }
-    fn = g_encode_tiled;
-    return SMLA_OK;
-}
-
-// Q [B*64 rows, 512 bf16] as a 2-D tensor; a box of 64 dims x 64 heads with the
-// 128-byte swizzle lands as one K-block of the shared-memory Q operand.
-int encode_q_map(CUtensorMap *map, const void *q, int B) {
-    PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    const int rc = tensor_map_encoder(fn);
-    if (rc != SMLA_OK) return rc;
-    cuuint64_t dims[2] = {static_cast<cuuint64_t>(SMLA_DIM), static_cast<cuuint64_t>(B) * SMLA_HEADS};
-    cuuint64_t strides[1] = {static_cast<cuuint64_t>(SMLA_DIM) * 2};
-    cuuint32_t box[2] = {64, 64};
-    cuuint32_t estr[2] = {1, 1};
-    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(q), dims, strides, box, estr,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? SMLA_OK : SMLA_ERR_INVALID;
-}
-
 int device_info(DeviceInfo *&info) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return SMLA_ERR_CUDA;
@@ -1201,8 +1109,6 @@ bool sizes_ok(int B, int H, int topk) {
     return B >= 1 && B <= 65535 && H == SMLA_HEADS && topk >= 1 && topk <= SMLA_MAX_TOPK;
 }
 
-size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
-
 // Two splits of a request merge inside the decode kernel (a CTA pair: the log-sum-exp
 // rows cross through distributed shared memory, the fp32 outputs are added into out);
 // more, or a bf16 output, go through normalised global partials and the merge kernel.
@@ -1218,8 +1124,6 @@ size_t workspace_for(int B, int topk, int nsplit) {
     (void)topk;
     return bytes;
 }
-
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 }  // namespace
 

@@ -1,0 +1,66 @@
+"""What the span operators and the cache reader refuse, without a GPU: the C entry points check
+sizes, pointers and alignment before they look for a device, the binding checks its tensors."""
+import ctypes
+
+import pytest
+import torch
+
+import sparse_mla_decode_fp8_b200 as smla
+from sparse_mla_decode_fp8_b200 import build
+
+INVALID = -1
+A, ODD, ODD16 = 1 << 20, (1 << 20) + 2, (1 << 20) + 8  # addresses that are never followed
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return smla.library()
+
+
+READ = [A, A, A, 5, A, 2, 3, 4, A, 1, A, None]
+KEYS = [A, A, A, A, A, 5, 2, 3, 4, A, A, None]
+SELECT = [A, 100, A, 8, 1, 1, A, A, 2, None]
+
+
+def _refused(fn, args, changes):
+    for at, bad in changes:
+        call = list(args)
+        call[at] = bad
+        assert fn(*call) == INVALID, (at, bad)
+
+
+def test_read_kv_refuses(lib):
+    _refused(lib.smla_read_kv, READ, [(0, None), (1, None), (2, None), (4, None), (8, None), (3, -1), (5, 0), (6, 0),
+                                      (7, 0), (7, 1 << 23), (0, ODD16), (8, ODD16), (1, ODD), (2, ODD), (4, ODD), (10, ODD)])
+    assert lib.smla_read_kv(None, None, None, 0, None, 1, 1, 1, None, 1, None, None) == 0  # nothing to read
+
+
+def test_span_keys_refuses(lib):
+    _refused(lib.smla_span_keys, KEYS, [(k, None) for k in (0, 1, 2, 3, 4, 9)] + [(5, -1), (6, 0), (7, 0), (8, 0),
+             (8, 1 << 23), (0, ODD16), (9, ODD16), (1, ODD), (2, ODD), (3, ODD), (4, ODD), (10, ODD)])
+    assert lib.smla_span_keys(None, None, None, None, None, 0, 1, 1, 1, None, None, None) == 0
+
+
+def test_select_spans_refuses(lib):
+    _refused(lib.smla_select_spans, SELECT, [(0, None), (2, None), (6, None), (1, 0), (1, (1 << 25) + 1), (3, 0), (3, 1025),
+             (4, -1), (5, -1), (4, 8), (5, 8), (4, 2**31 - 1), (8, 0), (0, ODD), (2, ODD), (6, ODD), (7, ODD)])
+
+
+def test_binding_refuses_host_tensors():
+    i = torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(smla.SmlaError):
+        smla.read_kv(torch.zeros((1, 149504), dtype=torch.uint8), i, i, i.view(1, 3))
+    with pytest.raises(smla.SmlaError):
+        smla.span_keys(torch.zeros((1, 149504), dtype=torch.uint8), i.view(1, 3), i[:1], i, i,
+                       torch.zeros((1, 4, 512), dtype=torch.bfloat16))
+    with pytest.raises(smla.SmlaError):
+        smla.select_spans(torch.zeros((3, 8)), i, 2)
+
+
+def test_entry_points_take_their_argument_counts(lib):
+    # every argument is described to ctypes: a call with one missing raises instead of running
+    for fn, args in ((lib.smla_read_kv, READ), (lib.smla_span_keys, KEYS), (lib.smla_select_spans, SELECT)):
+        assert len(fn.argtypes) == len(args)
+        with pytest.raises((TypeError, ctypes.ArgumentError)):
+            fn(*args[:-1])
