@@ -287,6 +287,37 @@ int smla_span_keys(const uint8_t *kv_cache, const int32_t *block_table, const in
 int smla_select_spans(const float *scores, int width, const int32_t *seq_lens, int nsel, int keep_first,
                       int keep_last, int32_t *spans, int32_t *topk_idx, int B, void *stream);
 
+/*
+ * smla_decode_spans -- attention of one new token per request over its whole cached
+ * sequence (spans NULL), or over the listed spans of it; the step of smla_decode with the
+ * tokens given by runs of 64 instead of one by one.
+ *   spans       device, int32 [B][nsel], or NULL with nsel 0.  Entries outside the request's
+ *               spans (-1 among them) hold no token; an entry listed twice counts twice;
+ *               1 <= nsel <= SMLA_MAX_NSEL
+ *   out         device, bf16 [B][H][512], 16-byte aligned (written): softmax weights enter the
+ *               second product as bf16, the sums are fp32, the result is rounded once
+ *   lse         device, fp32 [B][H] (written)
+ *   workspace   device scratch of at least smla_decode_spans_workspace_bytes(B) bytes, 256-byte
+ *               aligned, its first 4 bytes the sticky error word (see smla_decode).  Nothing
+ *               else in it has to start at zero.  Calls that may run at the same time, two
+ *               captured graphs among them, must not share one.
+ *   opts        NULL, or options with nsplit 0 and out_bf16 1 (wait_timeout_ns, debug_flags)
+ *   The other arguments are those of smla_decode.  A sequence longer than 256 max_blocks is
+ *   cut there.  A request without tokens gets out = 0, lse = -inf; tokens in a page outside
+ *   [0, num_pages) count for nothing and set SMLA_FLAG_BAD_PAGE.  A wait that ran out makes the
+ *   rows of the requests it touched NaN and sets SMLA_FLAG_TIMEOUT.
+ * Two launches on `stream`: the work of all requests is cut into equal parts over the SMs by
+ * the lengths on the device, then joined in a fixed order (reproducible bit for bit).
+ */
+int smla_decode_spans(const void *q, const uint8_t *kv_cache, const int32_t *block_table, const int32_t *spans,
+                      int nsel, const int32_t *seq_lens, float sm_scale, void *out, float *lse, int B, int H,
+                      int max_blocks, int num_pages, void *workspace, size_t workspace_bytes,
+                      const smla_options *opts, void *stream);
+
+/* Workspace bytes smla_decode_spans needs on the current device, for any lengths (39 MB on 148
+ * SMs, plus 8 B); 0 on a bad B or without an sm_100 device. */
+size_t smla_decode_spans_workspace_bytes(int B);
+
 /* Build identification string (static storage). */
 const char *smla_version(void);
 

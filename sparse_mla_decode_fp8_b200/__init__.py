@@ -16,6 +16,8 @@ from .binding import (  # noqa: F401
     combine,
     debug_gather,
     decode,
+    decode_spans,
+    decode_spans_workspace_bytes,
     library,
     num_splits,
     read_error,

@@ -26,6 +26,7 @@ DIM = 512
 PAGE_BYTES = 149504
 SPAN_TOKENS = 64
 PAGE_SPANS = 4
+MAX_NSEL = 1024
 
 _ERRORS = {-1: "invalid argument", -2: "unsupported device (needs sm_100)", -3: "CUDA runtime error",
            -4: "kernel launch failed"}
@@ -78,6 +79,11 @@ def library():
             lib.smla_span_keys.restype = I
             lib.smla_select_spans.argtypes = [P, I, P, I, I, I, P, P, I, P]
             lib.smla_select_spans.restype = I
+            lib.smla_decode_spans.argtypes = [P, P, P, P, I, P, ctypes.c_float, P, P, I, I, I, I, P, Z,
+                                              ctypes.POINTER(_Options), P]
+            lib.smla_decode_spans.restype = I
+            lib.smla_decode_spans_workspace_bytes.argtypes = [I]
+            lib.smla_decode_spans_workspace_bytes.restype = Z
             lib.smla_version.restype = ctypes.c_char_p
             _lib = lib
     return _lib
@@ -309,8 +315,8 @@ def select_spans(scores, seq_lens, nsel: int, keep_first: int = 0, keep_last: in
     dev = _device(scores, "scores")
     B, width = scores.shape if scores.dim() == 2 else (-1, -1)
     nsel, keep_first, keep_last = int(nsel), int(keep_first), int(keep_last)
-    if not 1 <= nsel <= 1024:
-        raise SmlaError("nsel must lie in [1, 1024]")
+    if not 1 <= nsel <= MAX_NSEL:
+        raise SmlaError(f"nsel must lie in [1, {MAX_NSEL}]")
     if spans is None:
         spans = _new(stream, (max(B, 0), nsel), torch.int32, dev)
     if topk_idx is None and tokens:
@@ -321,3 +327,55 @@ def select_spans(scores, seq_lens, nsel: int, keep_first: int = 0, keep_last: in
     rc = library().smla_select_spans(x, width, l, nsel, keep_first, keep_last, s, i, B, _stream(stream))
     _check(rc, "smla_select_spans")
     return spans, topk_idx
+
+
+def decode_spans_workspace_bytes(B: int) -> int:
+    n = library().smla_decode_spans_workspace_bytes(B)
+    if n == 0:
+        raise SmlaError("smla_decode_spans_workspace_bytes: invalid B or no sm_100 device")
+    return int(n)
+
+
+def decode_spans(q, kv_cache, block_table, seq_lens, sm_scale, spans=None, out=None, lse=None, workspace=None,
+                 wait_timeout_ns: int = 0, debug_flags: int = 0, stream=None):
+    """smla_decode_spans: (out bf16 [B,64,512], lse fp32 [B,64]) over the whole sequences, or
+    over ``spans`` (int32 [B,nsel]) of them.  Without a ``workspace`` one is allocated for the
+    call (and its error word is lost)."""
+    dev = _device(q, "q")
+    B = q.shape[0] if q.dim() == 3 else -1
+    nsel = 0
+    if spans is not None:
+        nsel = spans.shape[1] if isinstance(spans, torch.Tensor) and spans.dim() == 2 else -1
+        if not 1 <= nsel <= MAX_NSEL:  # an empty list is not "every span"
+            raise SmlaError(f"spans must be [B, nsel] with nsel in [1, {MAX_NSEL}]")
+    if out is None:
+        out = _new(stream, (max(B, 0), HEADS, DIM), torch.bfloat16, dev)
+    if lse is None:
+        lse = _new(stream, (max(B, 0), HEADS), torch.float32, dev)
+    x, c, t, l, s, o, e = _args(
+        dev, (q, torch.bfloat16, (B, HEADS, DIM), "q"), (kv_cache, torch.uint8, (None, PAGE_BYTES), "kv_cache"),
+        (block_table, torch.int32, (B, None), "block_table"), (seq_lens, torch.int32, (B,), "seq_lens"),
+        (spans, torch.int32, (B, nsel), "spans"), (out, torch.bfloat16, (B, HEADS, DIM), "out"),
+        (lse, torch.float32, (B, HEADS), "lse"))
+    if workspace is None:
+        workspace = _new(stream, decode_spans_workspace_bytes(B), torch.uint8, dev)
+        # only the error word has to start at zero
+        _zero_error_word(workspace, stream)
+    w, = _args(dev, (workspace, torch.uint8, None, "workspace"))
+    opts = None
+    if wait_timeout_ns or debug_flags:
+        opts = ctypes.byref(_Options(0, 1, wait_timeout_ns, debug_flags, 0))
+    rc = library().smla_decode_spans(x, c, t, s, nsel, l, float(sm_scale), o, e, B, HEADS, block_table.shape[1],
+                                     kv_cache.shape[0], w, workspace.numel(), opts, _stream(stream))
+    _check(rc, "smla_decode_spans")
+    return out, lse
+
+
+def _zero_error_word(workspace, stream) -> None:
+    if stream is None:
+        workspace[:4].zero_()
+        return
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream), device=workspace.device)
+    with torch.cuda.stream(stream):
+        workspace[:4].zero_()

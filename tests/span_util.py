@@ -85,3 +85,40 @@ def select(score_rows, seq_lens, nsel, first, last):
             t = np.arange(j * SPAN, (j + 1) * SPAN)
             idx[b, i * SPAN:(i + 1) * SPAN] = np.where(t < seq_lens[b], t, -1)
     return spans, idx
+
+
+def attention(q, cache, table, b, pos, sm_scale):
+    """fp64 attention of q [64, 512] over the listed positions of request b (with multiplicity):
+    (out, lse, weighted mean of |k|, largest sum |q k| sm_scale over the tokens)."""
+    if not len(pos):
+        z = np.zeros((64, 512))
+        return z, np.full(64, -np.inf), z, 0.0
+    k = latents(cache, table, b, pos)
+    s = sm_scale * (q @ k.T)
+    m = s.max(axis=1, keepdims=True)
+    p = np.exp(s - m)
+    total = p.sum(axis=1, keepdims=True)
+    size = abs(sm_scale) * float((np.abs(q) @ np.abs(k).T).max())
+    return p @ k / total, (m + np.log(total))[:, 0], p @ np.abs(k) / total, size
+
+
+def check_decode(out, lse, q, cache, table, positions, sm_scale):
+    """decode_spans' results against attention() over positions[b], with the bounds its arithmetic gives.
+
+    Scores: 512 exact bf16 products added in fp32, each addition off by at most 2^-23 of the largest
+    partial sum (the tensor core may truncate): |ds| <= 512 2^-23 size.  A weight's relative error is then
+    at most e = |ds| (of the token and of the reference m, which cancels in O and LSE up to rounding)
+    + 2^-21 (exp2 and the product with log2 e).  Weights enter P V as bf16, half a step 2^-8 each; the
+    sum over n tokens adds n 2^-23 of sum p |k|; the output is rounded once, 2^-8 of |O|."""
+    out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    for b, pos in enumerate(positions):
+        o, l, mean_abs, size = attention(q[b], cache, table, b, pos, sm_scale)
+        if not len(pos):
+            assert not out[b].any() and np.isneginf(lse[b]).all(), b
+            continue
+        n = len(pos)
+        e = 512 * 2.0 ** -23 * size + 2.0 ** -21
+        off = np.abs(out[b] - o)
+        bound = mean_abs * (2.0 ** -8 * (1 + 2 * e) + 2 * e + (n + 16) * 2.0 ** -23) + 2.0 ** -8 * (np.abs(o) + off)
+        assert (off <= bound).all(), (b, float((off - bound).max()))
+        assert (np.abs(lse[b] - l) <= e + (n + 16) * 2.0 ** -24 + 2.0 ** -21 * (1 + np.abs(l))).all(), b

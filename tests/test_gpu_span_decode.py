@@ -1,0 +1,220 @@
+"""smla_decode_spans through the binding against 64-bit attention (needs a B200): whole sequences and
+listed spans, ragged batches, empty requests, bad pages, streams, graphs and waits that run out.
+The caches are NaN bytes wherever no request has a token."""
+import numpy as np
+import pytest
+import torch
+
+import sparse_mla_decode_fp8_b200 as smla
+from sparse_mla_decode_fp8_b200 import build
+from tests import independent
+from tests import span_util as U
+from sparse_mla_decode_fp8_b200 import workloads as W
+
+pytestmark = pytest.mark.gpu
+SCALE = 512 ** -0.5
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    assert torch.cuda.is_available()
+    build.build()
+    smla.library()
+
+
+def _queries(B, seed):
+    return W.to_bf16_bits(np.random.default_rng(seed).standard_normal((B, 64, 512)).astype(np.float32))
+
+
+def _workspace(B):
+    # everything but the error word may hold anything
+    ws = torch.full((smla.decode_spans_workspace_bytes(B),), 0xFF, dtype=torch.uint8, device="cuda")
+    ws[:4] = 0
+    return ws
+
+
+def _run(lens, seed, spans=None, sm_scale=SCALE, **kw):
+    cache, table = U.paged(lens, seed)
+    qb = _queries(len(lens), seed)
+    ws = _workspace(len(lens))
+    out, lse = smla.decode_spans(U.dev_bf16(qb), U.dev(cache), U.dev(table), U.dev(np.asarray(lens, np.int32)), sm_scale,
+                                 spans=None if spans is None else U.dev(np.asarray(spans, np.int32)), workspace=ws, **kw)
+    torch.cuda.synchronize()
+    assert smla.read_error(ws) == 0
+    positions = []
+    for b, n in enumerate(lens):
+        if spans is None:
+            positions.append(np.arange(max(n, 0)))
+        else:
+            p = (np.asarray(spans[b], np.int64)[:, None] * 64 + np.arange(64)).reshape(-1)
+            positions.append(p[(p >= 0) & (p < n)])
+    U.check_decode(out, lse, independent.q_values(qb), cache, table, positions, sm_scale)
+    return out, lse
+
+
+@pytest.mark.parametrize("length", [1, 2, 63, 64, 65, 127, 128, 129, 255, 256, 257, 300, 1000])
+def test_one_request(length):
+    _run([length], seed=length)
+
+
+def test_one_long_request_over_every_sm():
+    _run([40000], seed=1)
+
+
+@pytest.mark.parametrize("lens", [[0], [0, 0, 5, 0], [-7, 300], [130, 0, 1, 64, 129, 0, 0, 2000, 31],
+                                  [1500, 1, 1, 700, 3000, 128, 256, 384]])
+def test_ragged(lens):
+    _run(lens, seed=len(lens) + lens[-1])
+
+
+def test_more_requests_than_sms():
+    rng = np.random.default_rng(3)
+    _run(list(rng.integers(0, 400, 333)), seed=3)
+
+
+def test_requests_of_several_tiles_inside_one_cta():
+    # 700 requests of 1..2 tiles: each CTA walks several whole ones
+    rng = np.random.default_rng(4)
+    _run(list(rng.integers(1, 200, 700)), seed=4)
+
+
+@pytest.mark.parametrize("sm_scale", [0.0, -SCALE, 8.0])
+def test_scales(sm_scale):
+    # 8: one token takes nearly all the weight, and the reference moves often
+    _run([777, 130], seed=5, sm_scale=sm_scale)
+
+
+def test_rising_scores_move_the_reference():
+    # later tokens point ever more along the query: every tile raises the maxima
+    n = 1300
+    cache, table = U.paged([n], seed=6)
+    qb = _queries(1, 6)
+    q = independent.q_values(qb)
+    mean = np.sign(q[0, 0]).astype(np.float32)
+    W.write_tokens(cache, table[0, np.arange(n) // 256].astype(np.int64), np.arange(n) % 256,
+                   (np.arange(n, dtype=np.float32)[:, None] / 20) * mean)
+    ws = _workspace(1)
+    out, lse = smla.decode_spans(U.dev_bf16(qb), U.dev(cache), U.dev(table), U.dev(np.array([n], np.int32)), 0.05, workspace=ws)
+    U.check_decode(out, lse, q, cache, table, [np.arange(n)], 0.05)
+
+
+@pytest.mark.parametrize("nsel", [1, 2, 3, 7, 32, 129])
+def test_listed_spans(nsel):
+    lens = [5000, 100, 0, 1, 4096, 20000]
+    rng = np.random.default_rng(nsel)
+    spans = np.full((len(lens), nsel), -1, np.int32)
+    for b, n in enumerate(lens):
+        have = -(-n // 64)
+        k = min(nsel, have)
+        spans[b, :k] = rng.choice(max(have, 1), k, replace=False)
+        rng.shuffle(spans[b])
+    _run(lens, seed=nsel, spans=spans)
+
+
+def test_listed_spans_repeat_and_out_of_range():
+    spans = [[3, 3, 0, -1, 3], [4, 5, 1 << 24, -5, 2**31 - 1], [-1, -1, -1, -1, -1], [0, 0, 0, 0, 0]]
+    _run([250, 257, 600, 0], seed=8, spans=spans)
+
+
+def test_a_sequence_longer_than_its_table_is_cut():
+    cache, table = U.paged([512], seed=9)
+    qb = _queries(1, 9)
+    ws = _workspace(1)
+    out, lse = smla.decode_spans(U.dev_bf16(qb), U.dev(cache), U.dev(table), U.dev(np.array([2**31 - 1], np.int32)), SCALE,
+                                 workspace=ws)
+    assert smla.read_error(ws) == 0
+    U.check_decode(out, lse, independent.q_values(qb), cache, table, [np.arange(512)], SCALE)
+
+
+def test_bad_pages_hold_no_tokens_and_are_reported():
+    lens = [700, 300, 256]
+    cache, table = U.paged(lens, seed=10)
+    table[0, 1], table[2, 0] = len(cache), -1
+    qb = _queries(3, 10)
+    ws = _workspace(3)
+    out, lse = smla.decode_spans(U.dev_bf16(qb), U.dev(cache), U.dev(table), U.dev(np.array(lens, np.int32)), SCALE, workspace=ws)
+    assert smla.read_error(ws) == smla.SMLA_FLAG_BAD_PAGE
+    U.check_decode(out, lse, independent.q_values(qb), cache, table,
+                   [np.r_[0:256, 512:700], np.arange(300), np.arange(0)], SCALE)
+
+
+def test_equals_the_sparse_decode_over_the_same_tokens():
+    lens, nsel = [3000, 900], 8
+    cache, table = U.paged(lens, seed=11)
+    qb = _queries(2, 11)
+    d = [U.dev(cache), U.dev(table)]
+    x = torch.rand((2, 48), device="cuda")
+    sl = U.dev(np.array(lens, np.int32))
+    spans, idx = smla.select_spans(x, sl, nsel, keep_first=1, keep_last=1)
+    out, lse = smla.decode_spans(U.dev_bf16(qb), *d, sl, SCALE, spans=spans)
+    ref, ref_lse = smla.decode(U.dev_bf16(qb), *d, idx, sl, SCALE)
+    assert (lse - ref_lse).abs().max() <= 1e-5 * (1 + ref_lse.abs().max())
+    assert (out.double() - ref.double()).norm() <= 5e-3 * ref.double().norm()
+
+
+def test_results_repeat_bit_for_bit_and_leave_other_rows():
+    lens = np.array([3001, 77, 0, 513], np.int32)
+    cache, table = U.paged(lens, seed=12)
+    qb = _queries(4, 12)
+    args = (U.dev_bf16(qb), U.dev(cache), U.dev(table), U.dev(lens), SCALE)
+    out = torch.full((6, 64, 512), 9.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((6, 64), 9.0, device="cuda")
+    first = [t.clone() for t in smla.decode_spans(*args, out=out[:4], lse=lse[:4], workspace=_workspace(4))]
+    assert (out[4:] == 9.0).all() and (lse[4:] == 9.0).all()
+    for _ in range(3):
+        again = smla.decode_spans(*args)
+        assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
+
+
+def test_another_stream_and_a_replayed_graph_with_new_lengths():
+    lens = np.array([900, 2000], np.int32)
+    cache, table = U.paged([2000, 2000], seed=13)
+    qb = _queries(2, 13)
+    q, c, t, sl = U.dev_bf16(qb), U.dev(cache), U.dev(table), U.dev(lens)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    out, lse = smla.decode_spans(q, c, t, sl, SCALE, stream=side)
+    side.synchronize()
+    qv = independent.q_values(qb)
+    U.check_decode(out, lse, qv, cache, table, [np.arange(n) for n in lens], SCALE)
+    ws = _workspace(2)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out, lse = smla.decode_spans(q, c, t, sl, SCALE, workspace=ws)
+    for lens in ([2000, 1], [0, 130], [5, 1999]):
+        sl.copy_(U.dev(np.array(lens, np.int32)))
+        g.replay()
+        torch.cuda.synchronize()
+        U.check_decode(out, lse, qv, cache, table, [np.arange(n) for n in lens], SCALE)
+
+
+@pytest.mark.parametrize("lens", [[100], [1000, 50], [40000, 1, 300]])
+def test_a_wait_that_runs_out_is_reported_and_leaves_nan_rows(lens):
+    # the first score MMAs signal a barrier nobody waits for: every CTA with tiles runs out of its 2 ms
+    cache, table = U.paged(lens, seed=14)
+    qb = _queries(len(lens), 14)
+    args = (U.dev_bf16(qb), U.dev(cache), U.dev(table), U.dev(np.array(lens, np.int32)), SCALE)
+    ws = _workspace(len(lens))
+    out, lse = smla.decode_spans(*args, workspace=ws, wait_timeout_ns=2_000_000, debug_flags=smla.SMLA_DEBUG_SKIP_FIRST_COMMIT)
+    torch.cuda.synchronize()
+    assert smla.read_error(ws) & smla.SMLA_FLAG_TIMEOUT
+    assert torch.isnan(out).all() and torch.isnan(lse).all()
+    out, lse = smla.decode_spans(*args, workspace=ws)
+    assert smla.read_error(ws) == 0
+    U.check_decode(out, lse, independent.q_values(qb), cache, table, [np.arange(n) for n in lens], SCALE)
+
+
+def test_refusals():
+    cache, table = U.paged([300], seed=15)
+    q, c, t = U.dev_bf16(_queries(1, 15)), U.dev(cache), U.dev(table)
+    sl = U.dev(np.array([300], np.int32))
+    for bad in (dict(spans=torch.zeros((2, 3), dtype=torch.int32, device="cuda")), dict(spans=torch.zeros((1, 0), dtype=torch.int32, device="cuda")),
+                dict(spans=torch.zeros((1, 1025), dtype=torch.int32, device="cuda")), dict(out=torch.empty((1, 64, 512), device="cuda")),
+                dict(lse=torch.empty((1, 63), device="cuda")), dict(workspace=torch.zeros(1000, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(smla.SmlaError):
+            smla.decode_spans(q, c, t, sl, SCALE, **bad)
+    for args in ((q.float(), c, t, sl), (q[:, :32], c, t, sl), (q, c[:, :-16], t, sl), (q, c, t.long(), sl), (q, c, t, sl.cpu())):
+        with pytest.raises(smla.SmlaError):
+            smla.decode_spans(*args, SCALE)
+    with pytest.raises(smla.SmlaError):
+        smla.decode_spans(q, c, t, sl, float("nan"))

@@ -20,6 +20,7 @@ def lib():
 
 READ = [A, A, A, 5, A, 2, 3, 4, A, 1, A, None]
 KEYS = [A, A, A, A, A, 5, 2, 3, 4, A, A, None]
+DECODE = [A, A, A, None, 0, A, 0.1, A, A, 2, 64, 3, 4, A, 1 << 30, None, None]
 SELECT = [A, 100, A, 8, 1, 1, A, A, 2, None]
 
 
@@ -47,6 +48,18 @@ def test_select_spans_refuses(lib):
              (4, -1), (5, -1), (4, 8), (5, 8), (4, 2**31 - 1), (8, 0), (0, ODD), (2, ODD), (6, ODD), (7, ODD)])
 
 
+def test_decode_spans_refuses(lib):
+    _refused(lib.smla_decode_spans, DECODE, [(k, None) for k in (0, 1, 2, 5, 7, 8, 13)] + [(4, 3), (4, -1), (6, float("nan")),
+             (6, float("inf")), (9, 0), (9, 65536), (10, 32), (11, 0), (12, 0), (12, 1 << 23), (0, ODD16), (1, ODD16),
+             (7, ODD16), (13, A + 128), (2, ODD), (3, ODD), (5, ODD), (8, ODD)])
+    listed = DECODE[:3] + [A] + DECODE[4:]
+    _refused(lib.smla_decode_spans, listed, [(4, 0), (4, 1025)])
+    for nsplit, out_bf16 in ((2, 1), (0, 0)):
+        opts = smla.binding._Options(nsplit, out_bf16, 0, 0, 0)
+        _refused(lib.smla_decode_spans, DECODE, [(15, ctypes.byref(opts))])
+    assert lib.smla_decode_spans_workspace_bytes(0) == 0 and lib.smla_decode_spans_workspace_bytes(65536) == 0
+
+
 def test_binding_refuses_host_tensors():
     i = torch.zeros(3, dtype=torch.int32)
     with pytest.raises(smla.SmlaError):
@@ -60,7 +73,8 @@ def test_binding_refuses_host_tensors():
 
 def test_entry_points_take_their_argument_counts(lib):
     # every argument is described to ctypes: a call with one missing raises instead of running
-    for fn, args in ((lib.smla_read_kv, READ), (lib.smla_span_keys, KEYS), (lib.smla_select_spans, SELECT)):
+    for fn, args in ((lib.smla_read_kv, READ), (lib.smla_span_keys, KEYS), (lib.smla_select_spans, SELECT),
+                     (lib.smla_decode_spans, DECODE)):
         assert len(fn.argtypes) == len(args)
         with pytest.raises((TypeError, ctypes.ArgumentError)):
             fn(*args[:-1])
