@@ -301,6 +301,7 @@ int smla_select_spans(const float *scores, int width, const int32_t *seq_lens, i
  *               aligned, its first 4 bytes the sticky error word (see smla_decode).  Nothing
  *               else in it has to start at zero.  Calls that may run at the same time, two
  *               captured graphs among them, must not share one.
+ *   kv_cache    32-byte aligned here
  *   opts        NULL, or options with nsplit 0 and out_bf16 1 (wait_timeout_ns, debug_flags)
  *   The other arguments are those of smla_decode.  A sequence longer than 256 max_blocks is
  *   cut there.  A request without tokens gets out = 0, lse = -inf; tokens in a page outside

@@ -18,8 +18,16 @@
 // a captured graph serves any lengths.  A request inside one CTA's range is finished by it;
 // the others leave parts (at most two per CTA) that the join kernel adds in a fixed order.
 //
-// Roles (16 warps): 8 warps dequantise, 4 run the softmax and the epilogue, one thread
-// issues the MMAs, one warp walks the CTA's range and publishes a tile's pages in a ring.
+// Roles (28 warps): four warpgroups dequantise, one 128-dim chunk of the tile each; two run the
+// softmax and the epilogue; of the last, one warp issues the MMAs and one walks the CTA's range and
+// publishes a tile's pages in a ring.
+//
+// What bounds it (64 requests of 65536 tokens, 950 us: 2.6 TB/s, 580 TFLOP/s; a tile takes 7,700
+// cycles): shared memory's port.  The MMAs of a tile read 128 bytes a cycle for 3,100 cycles, the
+// conversions store for 1,000, and the loads of the raw rows take the same pipe a cycle for 32 bytes,
+// 2,300: without them a tile takes 5,900.  They cannot come by TMA, since Q, the tile and P^T
+// leave no room for raw rows: tiles of 96 tokens that do leave it (and whose scores still take
+// MMAs of 128 rows) took 1,140 us, rope values alone by TMA with 16-byte loads of the rest 1,120.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -34,35 +42,42 @@ namespace smla {
 namespace span_decode {
 
 constexpr int kSpan = SMLA_SPAN_TOKENS;
-constexpr int kDequantWarps = 8;
-constexpr int kSoftmaxWarps = 4;
+constexpr int kChunks = 4;                        // dims chunks of 128, a dequantising warpgroup each
+constexpr int kDequantWarps = 4 * kChunks;
+constexpr int kSoftmaxWarps = 8;
 constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
-constexpr int kMmaWarp = kDequantWarps + kSoftmaxWarps;  // 12
-constexpr int kWalkWarp = kMmaWarp + 1;                  // 13
-constexpr int kThreads = 512;                            // 16 warps: 128 registers a thread
+constexpr int kMmaWarp = kDequantWarps + kSoftmaxWarps;  // 24
+constexpr int kWalkWarp = kMmaWarp + 1;                  // 25
+constexpr int kThreads = 32 * (kDequantWarps + kSoftmaxWarps + 4);
+// Registers a thread: 72 at launch (896 threads); the control warps give to those that dequantise.
+constexpr int kRegsLaunch = 72, kRegsNope = 80, kRegsRope = 80, kRegsSoftmax = 72, kRegsControl = 40;
+static_assert(32 * ((kDequantWarps - 4) * kRegsNope + 4 * kRegsRope + kSoftmaxWarps * kRegsSoftmax + 4 * kRegsControl) <=
+                  kThreads * kRegsLaunch && kThreads * kRegsLaunch <= 65536,
+              "the shares are drawn from what the block was launched with");
 constexpr int kRing = 4;                                 // tiles published ahead
 constexpr uint32_t kBarIdSoftmax = 1;                    // named barrier of the softmax warps
 constexpr float kRescaleThreshold = 64.0f;               // log2 units
-constexpr int kCombineThreads = 256;
+constexpr int kJoinWarps = 8;
 
 // Dynamic shared memory map (bytes from a 1024-aligned base).
 constexpr int kSmemQ = 0;                          // 64 KB: 8 K-blocks x [64 heads x 128 B], TMA-written
 constexpr int kSmemKV = kSmemQ + 65536;            // 128 KB: 8 K-blocks x [128 tokens x 128 B]
 constexpr int kSmemP = kSmemKV + 131072;           // 16 KB: P^T [128 tokens x 64 heads] bf16
 constexpr int kSmemRing = kSmemP + 16384;          // [kRing] Tile
-constexpr int kSmemRed = kSmemRing + kRing * 32;   // [4][64] f32: per-quadrant maxima or sums
+constexpr int kSmemScales = kSmemRing + kRing * 32;  // [kRing][128] scale rows of 8 bytes
+constexpr int kSmemRed = kSmemScales + kRing * 1024;   // [4][64] f32: per-quadrant maxima or sums
 constexpr int kSmemHeadM = kSmemRed + 1024;        // [64] m per head
 constexpr int kSmemAlpha = kSmemHeadM + 256;       // [64] rescale factors; 1/L in the epilogue
-constexpr int kSmemScan = kSmemAlpha + 256;        // block scan of the tile counts: [16] + 4 int64
-constexpr int kSmemBars = kSmemScan + 160;
+constexpr int kSmemScan = kSmemAlpha + 256;        // block scan of the tile counts (a row per warp), the range's start
+constexpr int kSmemBars = kSmemScan + 8 * (kThreads / 32 + 2);
 enum Bar : int {
     kBarRingFull = 0,               // + slot
     kBarRingEmpty = kRing,          // + slot: dequant warps, softmax warps and the MMA thread are done with it
     kBarQ = 2 * kRing,              // Q of the current request landed
-    kBarKvFull = kBarQ + 1,         // + dims chunk c: chunk written (8 warps)
+    kBarKvFull = kBarQ + 1,         // + dims chunk c: chunk written (4 warps)
     kBarKvFree = kBarKvFull + 4,    // + c: the PV of chunk c is done
     kBarS = kBarKvFree + 4,         // S^T of the tile complete
-    kBarP = kBarS + 1,              // P^T written (4 warps)
+    kBarP = kBarS + 1,              // P^T written (8 warps)
     kBarDrain = kBarP + 1,
     kBarSpare = kBarDrain + 1,      // test hook target
     kNumBars = kBarSpare + 1,
@@ -77,6 +92,7 @@ static_assert(kSmemBytes <= 232448, "exceeds the 227 KB per-block shared memory 
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 256;
 constexpr uint32_t kTmemL = 320;
+constexpr uint32_t kTmemPark = 384;  // converted rows of the next tile, 32 columns a warp
 
 extern __shared__ __align__(1024) uint8_t g_smem[];
 
@@ -121,11 +137,10 @@ __device__ __forceinline__ volatile int *sm_abort() { return reinterpret_cast<vo
 
 // Bounded wait on an mbarrier phase: false when the CTA has been aborted or the time is out
 // (which aborts it and sets the error word).
-__device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, const Params &p) {
+__device__ __forceinline__ bool wait_slow(uint64_t *bar, uint32_t parity, const Params &p) {
     const uint64_t t0 = global_timer_ns();
-    for (uint32_t k = 1;; ++k) {
-        if (mbar_test_wait(bar, parity)) return true;
-        if ((k & 31u) != 0) continue;
+    for (;;) {
+        if (mbar_try_wait_for(bar, parity, 1000000u)) return true;  // suspends for a bounded time
         if (*sm_abort()) return false;
         if (global_timer_ns() - t0 > p.timeout_ns) {
             *sm_abort() = 1;
@@ -137,13 +152,9 @@ __device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, const Par
 __device__ __forceinline__ bool wait_bar(int bar, uint32_t parity, const Params &p) {
     return mbar_test_wait(sm_bar(bar), parity) || wait_slow(sm_bar(bar), parity, p);
 }
-// Lane 0 waits, the warp follows.
-__device__ __forceinline__ bool warp_wait(int bar, uint32_t parity, const Params &p, int lane) {
-    int ok = 1;
-    if (lane == 0) ok = wait_bar(bar, parity, p) ? 1 : 0;
-    ok = __shfl_sync(0xffffffffu, ok, 0);
-    __syncwarp();  // orders the other lanes after lane 0's observation
-    return ok != 0;
+// Every lane waits; a uniform verdict.
+__device__ __forceinline__ bool all_wait(int bar, uint32_t parity, const Params &p) {
+    return __all_sync(0xffffffffu, wait_bar(bar, parity, p)) != 0;
 }
 
 // Number of tiles of request b.
@@ -199,8 +210,8 @@ __device__ __forceinline__ Range find_range(const Params &p, int tid) {
             if (r.begin < at + n) break;
             at += n;
         }
-        scan[16] = b;
-        scan[17] = r.begin - at;
+        scan[kThreads / 32] = b;
+        scan[kThreads / 32 + 1] = r.begin - at;
     }
     if (blockIdx.x == 0) {
         long long at = before;
@@ -211,8 +222,8 @@ __device__ __forceinline__ Range find_range(const Params &p, int tid) {
         if (tid == 0) p.prefix[p.B] = total;
     }
     __syncthreads();
-    r.b = r.begin < r.end ? static_cast<int>(scan[16]) : p.B;
-    r.at = r.begin < r.end ? scan[17] : 0;
+    r.b = r.begin < r.end ? static_cast<int>(scan[kThreads / 32]) : p.B;
+    r.at = r.begin < r.end ? scan[kThreads / 32 + 1] : 0;
     return r;
 }
 
@@ -235,6 +246,14 @@ __device__ __forceinline__ void span_code(const Params &p, int b, int len, long 
     }
     code = page * (kPageTokens / kSpan) + static_cast<int>(j % (kPageTokens / kSpan));
     count = static_cast<int>(min(static_cast<long long>(kSpan), len - j * kSpan));
+}
+
+// Waits for the scale rows of the tiles published last (the CTA was aborted: nobody else does).
+__device__ __forceinline__ void drain_scales(const Params &p, int k, int lane) {
+    if (lane == 0)
+        for (int i = max(0, k - kRing); i < k; ++i)
+            (void)mbar_wait(sm_bar(kBarRingFull + i % kRing), (i / kRing) & 1, p.timeout_ns);
+    __syncwarp();
 }
 
 __device__ __forceinline__ void walk(const Params &p, const Range &r, int lane) {
@@ -260,7 +279,7 @@ __device__ __forceinline__ void walk(const Params &p, const Range &r, int lane) 
             }
             const int m = static_cast<int>(min(32ll, n - base));
             for (int i = 0; i < m; ++i, ++k) {
-                if (!warp_wait(kBarRingEmpty + k % kRing, ((k / kRing) & 1) ^ 1, p, lane)) return;
+                if (!all_wait(kBarRingEmpty + k % kRing, ((k / kRing) & 1) ^ 1, p)) return drain_scales(p, k, lane);
                 if (lane == i) {
                     Tile t;
                     t.code[0] = code[0];
@@ -272,16 +291,19 @@ __device__ __forceinline__ void walk(const Params &p, const Range &r, int lane) 
                     t.part = part;
                     t.pad = 0;
                     sm_ring()[k % kRing] = t;
-                    mbar_arrive(sm_bar(kBarRingFull + k % kRing));
-                    // the rows head for L2 while the tiles before them are worked on
+                    // the scale rows come with the tile; the token rows head for L2 while the tiles
+                    // before them are worked on
+                    uint32_t bytes[2];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) bytes[u] = (count[u] * kScaleRowBytes + 15) & ~15;
+                    mbar_arrive_expect_tx(sm_bar(kBarRingFull + k % kRing), bytes[0] + bytes[1]);
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         if (code[u] < 0) continue;
-                        const uint8_t *rows = token_row(p.cache, code[u] * kSpan);
-                        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(rows), "r"(count[u] * kRowBytes)
-                                     : "memory");
-                        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(token_scales(p.cache, code[u] * kSpan)),
-                                     "r"((count[u] * kScaleRowBytes + 15) & ~15)
+                        bulk_load(smem_addr(g_smem + kSmemScales) + (k % kRing) * 1024 + u * 512,
+                                  token_scales(p.cache, code[u] * kSpan), bytes[u], sm_bar(kBarRingFull + k % kRing));
+                        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(token_row(p.cache, code[u] * kSpan)),
+                                     "r"(count[u] * kRowBytes)
                                      : "memory");
                     }
                 }
@@ -289,7 +311,7 @@ __device__ __forceinline__ void walk(const Params &p, const Range &r, int lane) 
             }
         }
     }
-    if (!warp_wait(kBarRingEmpty + k % kRing, ((k / kRing) & 1) ^ 1, p, lane)) return;
+    if (!all_wait(kBarRingEmpty + k % kRing, ((k / kRing) & 1) ^ 1, p)) return drain_scales(p, k, lane);
     if (lane == 0) {
         sm_ring()[k % kRing].b = -1;
         mbar_arrive(sm_bar(kBarRingFull + k % kRing));
@@ -297,134 +319,217 @@ __device__ __forceinline__ void walk(const Params &p, const Range &r, int lane) 
 }
 
 // ------------------------------------------------------------------ dequantisation
-// Thread t works on the tokens (t >> 3) + 32 j (j = 0..3, the first two in the first span).
-// Dims chunks 0..2 (128 nope dims): 16-byte unit t & 7 of each token; chunk 3: nope unit
-// 24 + (t & 3) of two of them, and rope unit t & 7 of each.
-struct Rows {
-    uint4 nope[3][4];
-    uint4 nope3[2];
-    uint4 rope[4];
-    uint2 scales[4];
-};
-
+// Warpgroup c writes dims [128c, 128c + 128) of every tile: of c = 0..2 two nope groups, of c = 3
+// the last nope group and the rope values.  Thread t (0..127) of it works on the token rows
+// own + 32 j (j = 0..3, the first two in the first span) and the 32 bytes u = t & 3 of the chunk's
+// 128; for c = 3 on rope bytes 32 u.. of those rows and on 32 nope bytes of the two rows in span
+// h = u >> 1.
+//
+// own: a store phase is 8 lanes with 16 bytes each; the four lanes of a row would hit each
+// bank group twice (u and u + 2 write the same columns of two K-blocks), as would the next row's.
+// Lanes with h = 1 therefore take the row of the other parity, and the second four lanes a
+// row that differs in bits 0 and 1: 8 bank groups of the swizzled tile, for nope and rope.
+//
+// One chunk per warpgroup and not all four in turn: a warp that converts chunk c + 1 with loads for
+// chunk c just issued was measured to wait for those (12,500 cycles a tile).
 struct Source {
     const uint8_t *row[2];  // first token row of each span
-    const uint8_t *scale[2];
+    uint32_t scales;        // shared memory: the spans' scale rows, 512 bytes each
     int count[2];
 };
 
-__device__ __forceinline__ Source tile_source(const Params &p, const Tile &t) {
+__device__ __forceinline__ int half_of(int t) { return (t >> 1) & 1; }
+__device__ __forceinline__ int own_row(int t) {
+    const int g = t >> 2;
+    return (g & ~3) | (((g & 1) * 3) ^ ((g >> 1) & 1) ^ half_of(t));
+}
+
+__device__ __forceinline__ Source tile_source(const Params &p, int slot) {
+    const Tile &t = sm_ring()[slot];
     Source s;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-        const int code = max(0, t.code[u]) * kSpan;
-        s.row[u] = token_row(p.cache, code);
-        s.scale[u] = token_scales(p.cache, code);
+        s.row[u] = token_row(p.cache, max(0, t.code[u]) * kSpan);
         s.count[u] = t.count[u];
     }
+    s.scales = smem_addr(g_smem + kSmemScales) + slot * (kTile * kScaleRowBytes);
     return s;
 }
 
-__device__ __forceinline__ void load_chunk(int c, int t, const Source &s, Rows &r) {
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+// 32 e4m3 bytes times 2^(s-127) -> 32 bf16 as four 16-byte units.  A byte sign-extended to 16 bits and
+// moved up by 4 has its sign, exponent and mantissa in bf16's places (0x87F0) and reads there as
+// the value times 2^-120, subnormals included; one multiplication by 2^(s-7) then gives the product
+// exactly (see smla.h for its range).  Three integer operations for two values: their pipe is
+// what bounds the conversion.  Above s = 134 that factor is no bf16, and a second one follows.
+__device__ __forceinline__ void convert_nope(const Bytes32 &raw, uint32_t s, uint4 (&v)[4]) {
+    const uint32_t m = (min(s, 134u) + 120u) * 0x00800080u;  // bf16 2^(s-7) in both halves
+    const uint32_t w[8] = {raw.a.x, raw.a.y, raw.a.z, raw.a.w, raw.b.x, raw.b.y, raw.b.z, raw.b.w};
+    uint32_t o[16];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int tok = (t >> 3) + 32 * (j & 1);
-        const bool valid = tok < s.count[j >> 1];
-        const uint8_t *row = s.row[j >> 1] + tok * kRowBytes + 16 * (t & 7);
-        if (c < 3)
-            r.nope[c][j] = valid ? ld_stream_v4(row + 128 * c) : zero;
+    for (int i = 0; i < 16; ++i) {
+        uint32_t two;  // prmt selectors with bit 3 set repeat the byte's sign
+        if (i & 1)
+            asm("prmt.b32 %0, %1, 0, 0xB3A2;" : "=r"(two) : "r"(w[i >> 1]));
         else
-            r.rope[j] = valid ? ld_stream_v4(row + kNope) : zero;
-        if (c == 3) r.scales[j] = valid ? ld_stream_v2(s.scale[j >> 1] + tok * kScaleRowBytes) : make_uint2(0u, 0u);
+            asm("prmt.b32 %0, %1, 0, 0x9180;" : "=r"(two) : "r"(w[i >> 1]));
+        o[i] = bf16x2_mul((two << 4) & 0x87F087F0u, m);
     }
-    if (c == 3) {
-        const int h = (t >> 2) & 1;  // lanes 4..7 of a group take the second span's tokens
+    if (s > 134u) {
+        const uint32_t m2 = s == 255u ? 0x7FC07FC0u : (s - 7u) * 0x00800080u;  // NaN, or 2^(s-134)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int tok = (t >> 3) + 32 * k;
-            const uint8_t *row = (h ? s.row[1] : s.row[0]) + tok * kRowBytes + 384 + 16 * (t & 3);
-            r.nope3[k] = tok < (h ? s.count[1] : s.count[0]) ? ld_stream_v4(row) : zero;
-        }
+        for (int i = 0; i < 16; ++i) o[i] = bf16x2_mul(o[i], m2);
     }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+}
+// Units 4n..4n+3 of the row at shared address `row`, whose swizzle is `sw`.
+__device__ __forceinline__ void store_nope(uint32_t row, int n, int sw, const uint4 (&v)[4]) {
+    const uint32_t first = row + (((4 * n) ^ sw) << 4);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) sts_v4(first ^ (q << 4), v[q]);
 }
 
-// 16 e4m3 bytes into token row r of K-block kb, 16-byte units oc and oc + 1 of its bf16 row.  Odd
-// K-blocks store their high half first, so that the 8 lanes of a store phase hit 8 bank groups.
-__device__ __forceinline__ void store_nope(uint32_t kv, int r, int kb, int oc, const uint4 raw, uint32_t scale,
-                                           bool high_first) {
-    uint4 lo, hi;
-    dequant16(raw, scale, lo, hi);
-    const uint32_t row = kv + kb * (kTile * 128) + r * 128;
-    const int sw = r & 7, f = high_first ? 1 : 0;
-    sts_v4(row + (((oc + f) ^ sw) << 4), f ? hi : lo);
-    sts_v4(row + (((oc + 1 - f) ^ sw) << 4), f ? lo : hi);
+__device__ __forceinline__ Bytes32 load32(const uint8_t *src, bool valid) {
+    if (valid) return ld_stream_v8(src);
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    return Bytes32{zero, zero};
 }
 
-__device__ __forceinline__ void store_chunk(int c, int t, const Rows &r) {
-    const uint32_t kv = smem_addr(g_smem + kSmemKV);
-    const int k8 = t & 7, k4 = t & 3, h = (t >> 2) & 1;
-    if (c < 3) {
-        const int kb = 2 * c + h;
+__device__ __forceinline__ uint32_t load_scale(const Source &s, int half, int tok, int g, bool valid) {
+    uint32_t v = 0;
+    if (valid)
+        asm volatile("ld.shared.u8 %0, [%1];"
+                     : "=r"(v)
+                     : "r"(s.scales + half * (kSpan * kScaleRowBytes) + tok * kScaleRowBytes + g));
+    return v;
+}
+
+// Dims chunks 0..2.  A tile is converted a tile ahead: right after the tile before it is stored,
+// while the tensor core works through its scores (the conversions of 12 warps next to the softmax
+// made that 900 cycles longer), and half of the converted rows wait in tensor memory (32 columns a
+// warp), which leaves the registers for the loads of the tile after.  Between the release of a
+// chunk and its hand-over there are only stores.
+struct NopePart {
+    Bytes32 raw[4];
+    uint32_t scale[4];
+    uint4 v[2][4];  // of rows j = 0, 1; those of j = 2, 3 are in tensor memory
+
+    __device__ __forceinline__ void load(int c, int t, const Source &s) {
+        const int own = own_row(t);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            store_nope(kv, (t >> 3) + 32 * j, kb, 2 * k4, r.nope[c][j], scale_byte(r.scales[j], kb), h != 0);
-    } else {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const uint2 sc = h ? r.scales[2 + k] : r.scales[k];
-            store_nope(kv, (t >> 3) + 64 * h + 32 * k, 6, 2 * k4, r.nope3[k], scale_byte(sc, 6), h != 0);
+        for (int j = 0; j < 4; ++j) {
+            const int tok = own + 32 * (j & 1);
+            raw[j] = load32(s.row[j >> 1] + tok * kRowBytes + 128 * c + 32 * (t & 3), tok < s.count[j >> 1]);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int row = (t >> 3) + 32 * j;
-            sts_v4(kv + 7 * (kTile * 128) + row * 128 + ((k8 ^ (row & 7)) << 4), r.rope[j]);
+            const int tok = own + 32 * (j & 1);
+            scale[j] = load_scale(s, j >> 1, tok, 2 * c + half_of(t), tok < s.count[j >> 1]);
         }
+    }
+    __device__ __forceinline__ void convert(uint32_t park) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) convert_nope(raw[2 + j], scale[2 + j], v[j]);
+        tmem_st32(park, reinterpret_cast<const float *>(v));
+#pragma unroll
+        for (int j = 0; j < 2; ++j) convert_nope(raw[j], scale[j], v[j]);
+        tmem_wait_st();
+    }
+    __device__ __forceinline__ void store(int c, int t, uint32_t park) {
+        const int own = own_row(t);
+        const uint32_t row = smem_addr(g_smem + kSmemKV) + (2 * c + half_of(t)) * (kTile * 128) + own * 128;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) store_nope(row + 32 * 128 * j, t & 1, own & 7, v[j]);
+        tmem_ld32(park, reinterpret_cast<float *>(v));
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 2; ++j) store_nope(row + 32 * 128 * (2 + j), t & 1, own & 7, v[j]);
+    }
+};
+
+__device__ __forceinline__ void nope_role(const Params &p, uint32_t tmem, int c, int t, int q, int lane) {
+    const uint32_t park = tmem + (static_cast<uint32_t>(32 * q) << 16) + kTmemPark + 32 * c;
+    NopePart part;
+    // loads tile k, if there is one: 1, none: 0, a wait failed: -1
+    auto fetch = [&](int k) {
+        if (!all_wait(kBarRingFull + k % kRing, (k / kRing) & 1, p)) return -1;
+        if (sm_ring()[k % kRing].b < 0) return 0;
+        part.load(c, t, tile_source(p, k % kRing));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sm_bar(kBarRingEmpty + k % kRing));
+        return 1;
+    };
+    if (fetch(0) <= 0) return;
+    part.convert(park);
+    for (int k = 0;; ++k) {
+        const int more = fetch(k + 1);
+        if (more < 0) return;
+        if (k > 0 && !all_wait(kBarKvFree + c, (k - 1) & 1, p)) return;
+        part.store(c, t, park);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sm_bar(kBarKvFull + c));
+        if (!more) return;
+        part.convert(park);
     }
 }
 
-__device__ __forceinline__ void dequant_role(const Params &p, int t, int lane) {
-    Rows rows;
-    if (!warp_wait(kBarRingFull, 0, p, lane)) return;
-    Tile tile = sm_ring()[0];
-    if (tile.b < 0) return;
-    {
-        const Source s = tile_source(p, tile);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) load_chunk(3 - c, t, s, rows);
-    }
+// Dims chunk 3: the last nope group and the rope values, loaded once the tile before is stored.
+__device__ __forceinline__ void rope_role(const Params &p, int t, int lane) {
+    const int own = own_row(t), h = half_of(t), sw = own & 7;
+    const uint32_t base = smem_addr(g_smem + kSmemKV) + 6 * (kTile * 128) + own * 128;
+    Source s;
+    if (!all_wait(kBarRingFull, 0, p) || sm_ring()[0].b < 0) return;
+    s = tile_source(p, 0);
     for (int k = 0;; ++k) {
-        // the next tile's pages; this tile's loads are all issued
+        Bytes32 raw[2], rope[4];
+        uint32_t scale[2];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int tok = own + 32 * (j & 1);
+            rope[j] = load32(s.row[j >> 1] + tok * kRowBytes + kNope + 32 * (t & 3), tok < s.count[j >> 1]);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int tok = own + 32 * j;
+            const bool valid = tok < (h ? s.count[1] : s.count[0]);
+            raw[j] = load32((h ? s.row[1] : s.row[0]) + tok * kRowBytes + 384 + 32 * (t & 1), valid);
+            scale[j] = load_scale(s, h, tok, 6, valid);
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(sm_bar(kBarRingEmpty + k % kRing));
-        if (!warp_wait(kBarRingFull + (k + 1) % kRing, ((k + 1) / kRing) & 1, p, lane)) return;
-        tile = sm_ring()[(k + 1) % kRing];
-        const bool more = tile.b >= 0;
-        const Source s = tile_source(p, tile);
-        const bool live = more;
+        // the next tile's pages: what its loads need is in registers before this tile is stored
+        if (!all_wait(kBarRingFull + (k + 1) % kRing, ((k + 1) / kRing) & 1, p)) return;
+        const bool more = sm_ring()[(k + 1) % kRing].b >= 0;
+        s = tile_source(p, (k + 1) % kRing);
+        uint4 v[2][4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            if (k > 0 && !warp_wait(kBarKvFree + c, (k - 1) & 1, p, lane)) return;
-            store_chunk(c, t, rows);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(sm_bar(kBarKvFull + c));
-            // chunk 3's load also replaces the scales, which chunks 0..3 of this tile have used by then
-            if (live) load_chunk(c, t, s, rows);
+        for (int j = 0; j < 2; ++j) convert_nope(raw[j], scale[j], v[j]);
+        if (k > 0 && !all_wait(kBarKvFree + 3, (k - 1) & 1, p)) return;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) store_nope(base + (64 * h + 32 * j) * 128, t & 1, sw, v[j]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t first = base + kTile * 128 + 32 * 128 * j + (((2 * (t & 3)) ^ sw) << 4);
+            sts_v4(first, rope[j].a);
+            sts_v4(first ^ 16, rope[j].b);
         }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sm_bar(kBarKvFull + 3));
         if (!more) return;
     }
 }
 
-// ------------------------------------------------------------------ MMA issue (one thread)
+// ------------------------------------------------------------------ MMA issue (one warp)
+// The warp walks its loop converged, so that descriptors stay in uniform registers, and one
+// elected lane issues.
 __device__ __forceinline__ void issue_pv(uint32_t d, uint32_t a_lo, uint32_t b_lo, bool accumulate) {
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks) {  // 16 tokens a step, 2 KB apart in the MN-major V^T and P^T
         const uint32_t o = ks * (2048 >> 4);
-        if (ks == 0 && !accumulate)
-            mma_bf16_ss(d, desc_from(a_lo, kDescHi), desc_from(b_lo, kDescHi), kIdescPV, 0u);
-        else
-            mma_bf16_ss_acc(d, desc_from(a_lo + o, kDescHi), desc_from(b_lo + o, kDescHi), kIdescPV);
+        mma_bf16_ss(d, desc_from(a_lo + o, kDescHi), desc_from(b_lo + o, kDescHi), kIdescPV,
+                    (ks > 0 || accumulate) ? 1u : 0u);
     }
 }
 
@@ -439,87 +544,101 @@ __device__ __forceinline__ void mma_role(const Params &p, const CUtensorMap *tma
     const uint32_t kv = smem_addr(g_smem + kSmemKV);
     const uint32_t qk_a = desc_lo(kv, 16), qk_b = desc_lo(smem_addr(g_smem + kSmemQ), 16);
     const uint32_t pv_a = desc_lo(kv, kTile * 128), pv_b = desc_lo(smem_addr(g_smem + kSmemP), 8192);
-    bool ok = wait_bar(kBarRingFull, 0, p), spare_used = false;
+    const bool leader = elect_one();
+    bool spare_used = false, q_pending = false;
     int flags = 0, segments = 0;  // segments: Q loads issued
+    bool ok = all_wait(kBarRingFull, 0, p) && sm_ring()[0].b >= 0;
     if (ok) {
-        const int b = sm_ring()[0].b;
         flags = sm_ring()[0].flags;
-        mbar_arrive(sm_bar(kBarRingEmpty));
-        if (b < 0) ok = false;
-        if (ok) {
-            load_q(tmap_q, b);
-            segments = 1;
-        }
+        if (leader) load_q(tmap_q, sm_ring()[0].b);
+        __syncwarp();
+        if (leader) mbar_arrive(sm_bar(kBarRingEmpty));
+        segments = 1;
+        q_pending = true;
     }
-    bool q_pending = segments > 0;
     for (int k = 0; ok; ++k) {
         const uint32_t par = k & 1;
         if (flags & kFirst) {
-            ok = wait_bar(kBarQ, (segments - 1) & 1, p);
+            ok = all_wait(kBarQ, (segments - 1) & 1, p);
             if (!ok) break;
             q_pending = false;
         }
-#pragma unroll 1
-        for (int c = 0; c < 4 && ok; ++c) {
-            ok = wait_bar(kBarKvFull + c, par, p);
+        // two chunks at a time: a look at a barrier takes hundreds of cycles while MMAs run, more than the
+        // MMAs that are queued by then
+#pragma unroll
+        for (int c = 0; c < 4; c += 2) {
+            ok = all_wait(kBarKvFull + c, par, p) && all_wait(kBarKvFull + c + 1, par, p);
             if (!ok) break;
             tc_fence_after_sync();
-            issue_qk_chunk(tmem + kTmemS, qk_a + c * 2 * ((kTile * 128) >> 4), qk_b + c * 2 * (8192 >> 4), c == 0);
+            if (leader) {
+#pragma unroll
+                for (int e = c; e < c + 2; ++e)
+                    issue_qk_chunk(tmem + kTmemS, qk_a + e * 2 * ((kTile * 128) >> 4), qk_b + e * 2 * (8192 >> 4), e == 0);
+            }
+            __syncwarp();
         }
         if (!ok) break;
         const bool hook = k == 0 && (p.debug_flags & SMLA_DEBUG_SKIP_FIRST_COMMIT);
-        mma_commit(sm_bar(hook ? kBarSpare : kBarS));
+        if (leader) mma_commit(sm_bar(hook ? kBarSpare : kBarS));
+        __syncwarp();
         spare_used = spare_used || hook;
         // the next tile; a new request's Q is fetched as soon as this tile's scores are done
-        ok = wait_bar(kBarRingFull + (k + 1) % kRing, ((k + 1) / kRing) & 1, p);
+        ok = all_wait(kBarRingFull + (k + 1) % kRing, ((k + 1) / kRing) & 1, p);
         if (!ok) break;
         const int next_b = sm_ring()[(k + 1) % kRing].b, next_flags = sm_ring()[(k + 1) % kRing].flags;
-        mbar_arrive(sm_bar(kBarRingEmpty + (k + 1) % kRing));
+        __syncwarp();
+        if (leader) mbar_arrive(sm_bar(kBarRingEmpty + (k + 1) % kRing));
         if (next_b >= 0 && (next_flags & kFirst)) {
-            ok = wait_bar(kBarS, par, p);
+            ok = all_wait(kBarS, par, p);
             if (!ok) break;
-            load_q(tmap_q, next_b);
+            if (leader) load_q(tmap_q, next_b);
             ++segments;
             q_pending = true;
         }
-        ok = wait_bar(kBarP, par, p);
+        ok = all_wait(kBarP, par, p);
         if (!ok) break;
         tc_fence_after_sync();
-#pragma unroll 1
+#pragma unroll
         for (int c = 0; c < 4; ++c) {
-            issue_pv(tmem + 64 * c, pv_a + c * 2 * ((kTile * 128) >> 4), pv_b, !(flags & kFirst));
-            mma_commit(sm_bar(kBarKvFree + c));
+            if (leader) {
+                issue_pv(tmem + 64 * c, pv_a + c * 2 * ((kTile * 128) >> 4), pv_b, !(flags & kFirst));
+                mma_commit(sm_bar(kBarKvFree + c));
+            }
+            __syncwarp();
         }
         if (next_b < 0) break;
         flags = next_flags;
     }
     // every MMA and copy issued must be complete before tensor and shared memory are released
-    if (spare_used) (void)mbar_wait(sm_bar(kBarSpare), 0, p.timeout_ns);
-    if (q_pending) (void)mbar_wait(sm_bar(kBarQ), (segments - 1) & 1, p.timeout_ns);
-    mma_commit(sm_bar(kBarDrain));
-    (void)mbar_wait(sm_bar(kBarDrain), 0, p.timeout_ns);
+    if (leader) {
+        if (spare_used) (void)mbar_wait(sm_bar(kBarSpare), 0, p.timeout_ns);
+        if (q_pending) (void)mbar_wait(sm_bar(kBarQ), (segments - 1) & 1, p.timeout_ns);
+        mma_commit(sm_bar(kBarDrain));
+        (void)mbar_wait(sm_bar(kBarDrain), 0, p.timeout_ns);
+    }
+    __syncwarp();
 }
 
 // ------------------------------------------------------------------ softmax and epilogue
-// Warp q (0..3) owns tensor-memory lanes 32q..: tokens of S^T, dims of an O^T chunk.
-// Verdicts that the four warps must share go through their named barrier.
+// Warp (q, hf) of the 8 owns tensor-memory lanes 32q.. (tokens of S^T, dims of an O^T chunk) and
+// heads 32 hf...  Verdicts that the 8 warps must share go through their named barrier.
 
 // Raises the references to the tile's maxima and rescales what was accumulated by
 // 2^(m_old - m_new): on a segment's first tile, and when a score passes m by more than
 // kRescaleThreshold.
-__device__ __noinline__ void raise_max(const Params &p, uint32_t tmem_lane, int q, int lane, bool valid, bool first) {
-#pragma unroll 1
-    for (int half = 0; half < 2; ++half) {
+__device__ __forceinline__ void raise_max(const Params &p, uint32_t tmem_lane, int q, int hf, int lane, bool valid,
+                                          bool first) {
+    {
         float y[32];
-        tmem_ld32(tmem_lane + kTmemS + 32 * half, y);
+        tmem_ld32(tmem_lane + kTmemS + 32 * hf, y);
         tmem_wait_ld();
 #pragma unroll
         for (int h = 0; h < 32; ++h) y[h] = valid ? y[h] * p.scale_log2 : -INFINITY;
-        sm_red()[q * 64 + 32 * half + lane] = warp_transpose_reduce<true, 32>(y, lane);
+        sm_red()[q * 64 + 32 * hf + lane] = warp_transpose_reduce<true, 32>(y, lane);
     }
     named_barrier_sync(kBarIdSoftmax, kSoftmaxThreads);
-    const int t = 32 * q + lane;
-    if (t < kHeads) {
+    if (q == 0) {
+        const int t = 32 * hf + lane;
         const float *red = sm_red();
         const float tm = fmaxf(fmaxf(red[t], red[64 + t]), fmaxf(red[128 + t], red[192 + t]));
         const float mo = first ? -INFINITY : sm_head_m()[t];
@@ -531,10 +650,10 @@ __device__ __noinline__ void raise_max(const Params &p, uint32_t tmem_lane, int 
     if (first) return;  // nothing accumulated yet
     // the PV of the tile before is complete: the commit of this tile's scores covers it
 #pragma unroll 1
-    for (int g = 0; g < 20; ++g) {  // 16 columns at a time: O^T and then L
-        const uint32_t col = tmem_lane + (g < 16 ? 16 * g : kTmemL + 16 * (g - 16));
+    for (int g = 0; g < 10; ++g) {  // 16 columns at a time: the four chunks of O^T, then L
+        const uint32_t col = tmem_lane + 64 * (g >> 1) + 32 * hf + 16 * (g & 1) + (g < 8 ? 0u : kTmemL - 256u);
         float al[16], o[16];
-        load16(sm_alpha() + 16 * (g & 3), al);
+        load16(sm_alpha() + 32 * hf + 16 * (g & 1), al);
         tmem_ld16(col, o);
         tmem_wait_ld();
 #pragma unroll
@@ -545,17 +664,17 @@ __device__ __noinline__ void raise_max(const Params &p, uint32_t tmem_lane, int 
 }
 
 // L per head over the 128 lanes -> 1/L, and the segment's log-sum-exps.
-__device__ __noinline__ void finish_sums(const Params &p, uint32_t tmem_lane, int q, int lane, int b, int part) {
-#pragma unroll 1
-    for (int half = 0; half < 2; ++half) {
+__device__ __forceinline__ void finish_sums(const Params &p, uint32_t tmem_lane, int q, int hf, int lane, int b,
+                                            int part) {
+    {
         float y[32];
-        tmem_ld32(tmem_lane + kTmemL + 32 * half, y);
+        tmem_ld32(tmem_lane + kTmemL + 32 * hf, y);
         tmem_wait_ld();
-        sm_red()[q * 64 + 32 * half + lane] = warp_transpose_reduce<false, 32>(y, lane);
+        sm_red()[q * 64 + 32 * hf + lane] = warp_transpose_reduce<false, 32>(y, lane);
     }
     named_barrier_sync(kBarIdSoftmax, kSoftmaxThreads);
-    const int t = 32 * q + lane;
-    if (t < kHeads) {
+    if (q == 0) {
+        const int t = 32 * hf + lane;
         const float *red = sm_red();
         const float l = (red[t] + red[64 + t]) + (red[128 + t] + red[192 + t]);
         // l = 0: no valid token; NaN goes through
@@ -569,16 +688,18 @@ __device__ __noinline__ void finish_sums(const Params &p, uint32_t tmem_lane, in
     named_barrier_sync(kBarIdSoftmax, kSoftmaxThreads);
 }
 
-// O^T / L: dim 128c + 32q + lane of every head; a warp's stores of a head are contiguous.
-__device__ __noinline__ void write_out(const Params &p, uint32_t tmem_lane, int q, int lane, int b, int part) {
+// O^T / L: dim 128c + 32q + lane of this warp's heads; a warp's stores of a head are contiguous.
+__device__ __forceinline__ void write_out(const Params &p, uint32_t tmem_lane, int q, int hf, int lane, int b,
+                                          int part) {
     const size_t first = static_cast<size_t>(part >= 0 ? part : b) * kHeads * kDim + 32 * q + lane;
 #pragma unroll 1
-    for (int g = 0; g < 16; ++g) {  // dims chunk g / 4, heads 16 (g % 4)..
+    for (int g = 0; g < 8; ++g) {  // dims chunk g / 2, heads 32 hf + 16 (g % 2)..
+        const int h0 = 32 * hf + 16 * (g & 1);
         float o[16], inv[16];
-        tmem_ld16(tmem_lane + 16 * g, o);
-        load16(sm_alpha() + 16 * (g & 3), inv);
+        tmem_ld16(tmem_lane + 64 * (g >> 1) + h0, o);
+        load16(sm_alpha() + h0, inv);
         tmem_wait_ld();
-        const size_t at = first + 128 * (g >> 2) + static_cast<size_t>(16 * (g & 3)) * kDim;
+        const size_t at = first + 128 * (g >> 1) + static_cast<size_t>(h0) * kDim;
         if (part >= 0) {
 #pragma unroll
             for (int h = 0; h < 16; ++h) p.part_o[at + h * kDim] = o[h] * inv[h];
@@ -589,60 +710,59 @@ __device__ __noinline__ void write_out(const Params &p, uint32_t tmem_lane, int 
     }
 }
 
-__device__ __forceinline__ void softmax_role(const Params &p, uint32_t tmem, int q, int lane) {
+// Scores of this warp's heads in log2 units less the references (-inf for a masked token) and
+// their maximum.
+__device__ __forceinline__ float load_scores(uint32_t lane_addr, int hf, float c, bool whole, bool valid,
+                                             float (&x)[32]) {
+    tmem_ld32(lane_addr + kTmemS + 32 * hf, x);
+    tmem_wait_ld();
+#pragma unroll
+    for (int g = 0; g < 8; ++g) {
+        const float4 m = reinterpret_cast<const float4 *>(sm_head_m() + 32 * hf)[g];
+        x[4 * g] = fmaf(x[4 * g], c, -m.x);
+        x[4 * g + 1] = fmaf(x[4 * g + 1], c, -m.y);
+        x[4 * g + 2] = fmaf(x[4 * g + 2], c, -m.z);
+        x[4 * g + 3] = fmaf(x[4 * g + 3], c, -m.w);
+    }
+    if (!whole) {  // a tile with masked tokens: uniform over the warps
+#pragma unroll
+        for (int h = 0; h < 32; ++h) x[h] = valid ? x[h] : -INFINITY;
+    }
+    float top[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+    for (int h = 4; h < 32; ++h) top[h & 3] = fmaxf(top[h & 3], x[h]);
+    return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+}
+
+__device__ __forceinline__ void softmax_role(const Params &p, uint32_t tmem, int q, int hf, int lane) {
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * q) << 16);
     const int r = 32 * q + lane;  // token row
     const uint32_t prow = smem_addr(g_smem + kSmemP) + r * 128;
-    const float c = p.scale_log2;
     for (int k = 0;; ++k) {
         const uint32_t par = k & 1;
-        bool ok = warp_wait(kBarRingFull + k % kRing, (k / kRing) & 1, p, lane);
+        bool ok = all_wait(kBarRingFull + k % kRing, (k / kRing) & 1, p);
         const Tile tile = sm_ring()[k % kRing];
         const bool done = ok && tile.b < 0;  // leaves through the barriers below: another warp's wait may have failed
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(sm_bar(kBarRingEmpty + k % kRing));
         const bool first = tile.flags & kFirst;
-        const bool valid = (r & 63) < tile.count[(r >> 6) & 1];
-        ok = ok && !done && warp_wait(kBarS, par, p, lane);
+        const bool whole = tile.count[0] == kSpan && tile.count[1] == kSpan;
+        const bool valid = (r & 63) < ((r >> 6) ? tile.count[1] : tile.count[0]);
+        ok = ok && !done && all_wait(kBarS, par, p);
         tc_fence_after_sync();
-        float x[64];
+        float x[32];
         bool over = first || !ok;
-        if (ok) {
-            tmem_ld32(lane_addr + kTmemS, x);
-            tmem_ld32(lane_addr + kTmemS + 32, x + 32);
-            tmem_wait_ld();
-        }
-        if (!over) {
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                float m[16];
-                load16(sm_head_m() + 16 * g, m);
-#pragma unroll
-                for (int h = 0; h < 16; ++h) {
-                    x[16 * g + h] = valid ? fmaf(x[16 * g + h], c, -m[h]) : -INFINITY;
-                    over |= x[16 * g + h] > kRescaleThreshold;
-                }
-            }
-        }
+        if (!over) over = load_scores(lane_addr, hf, p.scale_log2, whole, valid, x) > kRescaleThreshold;
         if (barrier_or(kBarIdSoftmax, kSoftmaxThreads, over)) {
             if (barrier_or(kBarIdSoftmax, kSoftmaxThreads, !ok)) return;
-            raise_max(p, lane_addr, q, lane, valid, first);
-            tmem_ld32(lane_addr + kTmemS, x);
-            tmem_ld32(lane_addr + kTmemS + 32, x + 32);
-            tmem_wait_ld();
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                float m[16];
-                load16(sm_head_m() + 16 * g, m);
-#pragma unroll
-                for (int h = 0; h < 16; ++h) x[16 * g + h] = valid ? fmaf(x[16 * g + h], c, -m[h]) : -INFINITY;
-            }
+            raise_max(p, lane_addr, q, hf, lane, valid, first);
+            (void)load_scores(lane_addr, hf, p.scale_log2, whole, valid, x);
         }
 #pragma unroll
-        for (int h = 0; h < 64; ++h) x[h] = fast_exp2(x[h]);
+        for (int h = 0; h < 32; ++h) x[h] = fast_exp2(x[h]);
 #pragma unroll
-        for (int g = 0; g < 8; ++g)
-            sts_v4(prow + ((g ^ (r & 7)) << 4),
+        for (int g = 0; g < 4; ++g)
+            sts_v4(prow + (((4 * hf + g) ^ (r & 7)) << 4),
                    make_uint4(pack_bf16x2(x[8 * g], x[8 * g + 1]), pack_bf16x2(x[8 * g + 2], x[8 * g + 3]),
                               pack_bf16x2(x[8 * g + 4], x[8 * g + 5]), pack_bf16x2(x[8 * g + 6], x[8 * g + 7])));
         fence_proxy_async_smem();
@@ -651,26 +771,36 @@ __device__ __forceinline__ void softmax_role(const Params &p, uint32_t tmem, int
         if (lane == 0) mbar_arrive(sm_bar(kBarP));
         // L += p, after the hand-over: the PV does not read it
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
+        for (int g = 0; g < 2; ++g) {
+            const uint32_t col = lane_addr + kTmemL + 32 * hf + 16 * g;
             if (!first) {
                 float l[16];
-                tmem_ld16(lane_addr + kTmemL + 16 * g, l);
+                tmem_ld16(col, l);
                 tmem_wait_ld();
 #pragma unroll
                 for (int h = 0; h < 16; ++h) x[16 * g + h] += l[h];
             }
-            tmem_st16(lane_addr + kTmemL + 16 * g, x + 16 * g);
+            tmem_st16(col, x + 16 * g);
         }
         tmem_wait_st();
         if (tile.flags & kLast) {
-            ok = warp_wait(kBarKvFree + 3, par, p, lane);  // commits complete in order: every chunk of O^T is final
+            ok = all_wait(kBarKvFree + 3, par, p);  // commits complete in order: every chunk of O^T is final
             if (barrier_or(kBarIdSoftmax, kSoftmaxThreads, !ok)) return;
             tc_fence_after_sync();
-            finish_sums(p, lane_addr, q, lane, tile.b, tile.part);
-            write_out(p, lane_addr, q, lane, tile.b, tile.part);
+            finish_sums(p, lane_addr, q, hf, lane, tile.b, tile.part);
+            write_out(p, lane_addr, q, hf, lane, tile.b, tile.part);
             tc_fence_before_sync();
         }
     }
+}
+
+template <int kRegs>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -698,7 +828,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(sm_bar(kBarQ), 1);
         for (int c = 0; c < 4; ++c) {
-            mbar_init(sm_bar(kBarKvFull + c), kDequantWarps);
+            mbar_init(sm_bar(kBarKvFull + c), kDequantWarps / kChunks);
             mbar_init(sm_bar(kBarKvFree + c), 1);
         }
         mbar_init(sm_bar(kBarS), 1);
@@ -714,14 +844,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *tmem_slot;
 
     if (warp < kDequantWarps) {
-        dequant_role(p, tid, lane);
+        if (warp < kDequantWarps - 4) {
+            more_registers<kRegsNope>();
+            nope_role(p, tmem, warp >> 2, tid & 127, warp & 3, lane);
+        } else {
+            more_registers<kRegsRope>();
+            rope_role(p, tid & 127, lane);
+        }
     } else if (warp < kMmaWarp) {
-        softmax_role(p, tmem, warp - kDequantWarps, lane);
-    } else if (warp == kMmaWarp) {
-        if (lane == 0) mma_role(p, &tmap_q, tmem);
-        __syncwarp();
-    } else if (warp == kWalkWarp) {
-        walk(p, range, lane);
+        softmax_role(p, tmem, warp & 3, (warp - kDequantWarps) >> 2, lane);
+    } else {
+        fewer_registers<kRegsControl>();
+        if (warp == kMmaWarp)
+            mma_role(p, &tmap_q, tmem);
+        else if (warp == kWalkWarp)
+            walk(p, range, lane);
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -733,50 +870,62 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------ the join
-// Block (x, b) finishes heads [x heads_per, ..) of request b: zeros and -inf for a request without
-// tiles, NaN where a CTA gave up, nothing for a request that one CTA wrote whole, and
-// otherwise the parts, in the order of the CTAs, with weights 2^(lambda - max).
-__global__ void __launch_bounds__(kCombineThreads)
-    join_kernel(const __grid_constant__ Params p, int grid, int heads_per) {
-    const int b = blockIdx.y, t = threadIdx.x;
+// One warp per (request, head); blockIdx.x is the request and kJoinWarps heads.  Zeros and -inf for
+// a request without tiles, NaN where a CTA gave up, nothing for a request that one CTA wrote
+// whole, and otherwise the parts, in the order of the CTAs, with weights 2^(lambda - max).
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ Params p, int grid) {
+    const int b = blockIdx.x / (kHeads / kJoinWarps);
+    const int h = blockIdx.x % (kHeads / kJoinWarps) * kJoinWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     const long long begin = p.prefix[b], n = p.prefix[b + 1] - begin, total = p.prefix[p.B];
     const long long per = max(1ll, (total + grid - 1) / grid);
-    const int h0 = blockIdx.x * heads_per;
     const int c0 = static_cast<int>(begin / per), c1 = n > 0 ? static_cast<int>((begin + n - 1) / per) : c0 - 1;
-    int bad = 0;
-    for (int c = c0 + t; c <= c1; c += kCombineThreads) bad |= p.failed[c];
-    bad = __syncthreads_or(bad);
+    // part c of the request: lane c - c0 - 32 i looks at it
+    auto index = [&](int c) { return static_cast<size_t>(2 * c + (c == c0 && begin > c * per ? 1 : 0)) * kHeads + h; };
+    bool bad = false;
+    float top = -INFINITY;
+    for (int c = c0 + lane; c <= c1; c += 32) {
+        bad |= p.failed[c] != 0;
+        const float v = c0 < c1 ? p.part_lambda[index(c)] : 0.0f;
+        bad |= isnan(v);
+        top = fmaxf(top, v);
+    }
+    bad = __any_sync(0xffffffffu, bad);
     if (c0 == c1 && !bad) return;
-    uint32_t *out = reinterpret_cast<uint32_t *>(p.out + (static_cast<size_t>(b) * kHeads) * kDim);
-    for (int h = h0; h < h0 + heads_per; ++h) {
-        float top = -INFINITY, sum = 0.0f, x = 0.0f, y = 0.0f;
-        if (bad) {
-            x = y = NAN;
-        } else {
-            auto part = [&](int c) { return 2 * c + (c == c0 && begin > c * per ? 1 : 0); };
-            for (int c = c0; c <= c1; ++c) {
-                const float v = p.part_lambda[static_cast<size_t>(part(c)) * kHeads + h];
-                top = (isnan(v) || isnan(top)) ? NAN : fmaxf(top, v);
-            }
-            if (top != -INFINITY) {
-#pragma unroll 4
-                for (int c = c0; c <= c1; ++c) {
-                    const size_t at = static_cast<size_t>(part(c)) * kHeads + h;
-                    const float w = exp2f(p.part_lambda[at] - top);
-                    const float2 o = reinterpret_cast<const float2 *>(p.part_o + at * kDim)[t];
-                    sum += w;
-                    x += w * o.x;
-                    y += w * o.y;
-                }
-                x /= sum;
-                y /= sum;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = bad ? NAN : 0.0f;
+    float sum = 0.0f;
+    if (!bad && top != -INFINITY) {
+#pragma unroll 2
+        for (int c = c0; c <= c1; ++c) {
+            const size_t at = index(c);
+            const float4 *src = reinterpret_cast<const float4 *>(p.part_o + at * kDim) + lane;
+            float4 o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = src[32 * i];
+            const float w = exp2f(p.part_lambda[at] - top);
+            sum += w;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[4 * i] += w * o[i].x;
+                x[4 * i + 1] += w * o[i].y;
+                x[4 * i + 2] += w * o[i].z;
+                x[4 * i + 3] += w * o[i].w;
             }
         }
-        out[h * (kDim / 2) + t] = pack_bf16x2(x, y);
-        if (t == 0)
-            p.lse[static_cast<size_t>(b) * kHeads + h] =
-                bad ? NAN : top == -INFINITY ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+        const float inv = 1.0f / sum;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] *= inv;
     }
+    uint2 *dst = reinterpret_cast<uint2 *>(p.out + (static_cast<size_t>(b) * kHeads + h) * kDim) + lane;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        dst[32 * i] = make_uint2(pack_bf16x2(x[4 * i], x[4 * i + 1]), pack_bf16x2(x[4 * i + 2], x[4 * i + 3]));
+    if (lane == 0)
+        p.lse[static_cast<size_t>(b) * kHeads + h] =
+            bad ? NAN : top == -INFINITY ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
 }
 
 }  // namespace span_decode
@@ -834,7 +983,7 @@ int smla_decode_spans(const void *q, const uint8_t *kv_cache, const int32_t *blo
     if (B < 1 || B > 65535 || H != SMLA_HEADS || max_blocks < 1 || num_pages < 1 || num_pages >= (1 << 23))
         return SMLA_ERR_INVALID;
     if (spans ? (nsel < 1 || nsel > SMLA_MAX_NSEL) : nsel != 0) return SMLA_ERR_INVALID;
-    if (!aligned(q, 16) || !aligned(kv_cache, 16) || !aligned(out, 16) || !aligned(workspace, 256) ||
+    if (!aligned(q, 16) || !aligned(kv_cache, 32) || !aligned(out, 16) || !aligned(workspace, 256) ||
         !aligned(block_table, 4) || !aligned(spans, 4) || !aligned(seq_lens, 4) || !aligned(lse, 4))
         return SMLA_ERR_INVALID;
     if (!std::isfinite(sm_scale) || (opts && (opts->nsplit != 0 || opts->out_bf16 == 0))) return SMLA_ERR_INVALID;
@@ -872,8 +1021,7 @@ int smla_decode_spans(const void *q, const uint8_t *kv_cache, const int32_t *blo
     (void)cudaGetLastError();
     span_decode_kernel<<<static_cast<unsigned>(sms), kThreads, kSmemBytes, st>>>(p, tmap_q);
     if (cudaGetLastError() != cudaSuccess) return SMLA_ERR_LAUNCH;
-    const int heads_per = B >= 32 ? 8 : 1;
-    join_kernel<<<dim3(SMLA_HEADS / heads_per, static_cast<unsigned>(B)), kCombineThreads, 0, st>>>(p, sms, heads_per);
+    join_kernel<<<static_cast<unsigned>(B) * (SMLA_HEADS / kJoinWarps), 32 * kJoinWarps, 0, st>>>(p, sms);
     return cudaGetLastError() == cudaSuccess ? SMLA_OK : SMLA_ERR_LAUNCH;
 }
 
