@@ -273,6 +273,32 @@ int smla_span_keys(const uint8_t *kv_cache, const int32_t *block_table, const in
                    void *stream);
 
 /*
+ * smla_span_scores -- how much of a query's attention each span of its request should get,
+ * estimated from the span keys: score[b][j] = sum over the 64 heads of
+ * softmax_j(sm_scale <q[b][h], key_j>), the softmax over the request's spans; the scores of a
+ * request add up to 64.
+ *   q           device, bf16 [B][H][512], as for the decode that follows
+ *   keys        device, bf16 [num_pages][4][512], as smla_span_keys writes them
+ *   scores      device, fp32 [B][4 max_blocks] (written): 0 behind the request's last span; a
+ *               span in a page outside [0, num_pages) takes no part, scores 0 and sets
+ *               SMLA_FLAG_BAD_PAGE
+ *   workspace   device scratch of at least smla_span_scores_workspace_bytes(B, max_blocks)
+ *               bytes, 256-byte aligned, its first 4 bytes the sticky error word (see
+ *               smla_decode); not shared by calls that may run at the same time
+ *   opts        NULL, or options with nsplit 0 and out_bf16 0 (wait_timeout_ns, debug_flags); a
+ *               wait that ran out makes the scores of the requests it touched NaN
+ *   H must be 64; 1 <= max_blocks <= SMLA_MAX_SPANS / 4.  Two launches on `stream`; sums in a
+ *   fixed order (reproducible bit for bit).
+ */
+int smla_span_scores(const void *q, const void *keys, const int32_t *block_table, const int32_t *seq_lens,
+                     float sm_scale, float *scores, int B, int H, int max_blocks, int num_pages, void *workspace,
+                     size_t workspace_bytes, const smla_options *opts, void *stream);
+
+/* Workspace bytes smla_span_scores needs (about 1 KB per 4 spans of every request, any lengths); 0 on
+ * bad sizes. */
+size_t smla_span_scores_workspace_bytes(int B, int max_blocks);
+
+/*
  * smla_select_spans -- per request the nsel spans with the highest scores, among them always
  * its first keep_first and its last keep_last spans (0 <= keep_first + keep_last <= nsel).
  * Ties go to the lower span; NaN scores rank with -inf, below every number.

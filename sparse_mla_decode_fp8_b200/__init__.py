@@ -24,6 +24,8 @@ from .binding import (  # noqa: F401
     read_kv,
     select_spans,
     span_keys,
+    span_scores,
+    span_scores_workspace_bytes,
     version,
     workspace_bytes,
     write_kv,

@@ -84,6 +84,10 @@ def library():
             lib.smla_decode_spans.restype = I
             lib.smla_decode_spans_workspace_bytes.argtypes = [I]
             lib.smla_decode_spans_workspace_bytes.restype = Z
+            lib.smla_span_scores.argtypes = [P, P, P, P, ctypes.c_float, P, I, I, I, I, P, Z, ctypes.POINTER(_Options), P]
+            lib.smla_span_scores.restype = I
+            lib.smla_span_scores_workspace_bytes.argtypes = [I, I]
+            lib.smla_span_scores_workspace_bytes.restype = Z
             lib.smla_version.restype = ctypes.c_char_p
             _lib = lib
     return _lib
@@ -251,15 +255,30 @@ def _device(t, name) -> torch.device:
     return t.device
 
 
+def _as_stream(stream, device) -> torch.cuda.Stream:
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(_stream(stream), device=device)
+
+
 def _new(stream, shape, dtype, device, zero=False) -> torch.Tensor:
     """A tensor allocated on the stream that will write it."""
     make = torch.zeros if zero else torch.empty
     if stream is None:
         return make(shape, dtype=dtype, device=device)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_stream(stream), device=device)
-    with torch.cuda.stream(stream):
+    with torch.cuda.stream(_as_stream(stream, device)):
         return make(shape, dtype=dtype, device=device)
+
+
+def _scratch(nbytes: int, device, stream) -> torch.Tensor:
+    """A workspace for one call: only the error word has to start at zero."""
+    ws = _new(stream, nbytes, torch.uint8, device)
+    if stream is None:
+        ws[:4].zero_()
+    else:
+        with torch.cuda.stream(_as_stream(stream, device)):
+            ws[:4].zero_()
+    return ws
 
 
 def _err(err, device):
@@ -306,6 +325,39 @@ def span_keys(kv_cache, block_table, seq_lens, req, span, keys, err=None, stream
     rc = library().smla_span_keys(c, t, l, r, s, n, B, blocks, pages, k, _err(err, dev), _stream(stream))
     _check(rc, "smla_span_keys")
     return keys
+
+
+def span_scores_workspace_bytes(B: int, max_blocks: int) -> int:
+    n = library().smla_span_scores_workspace_bytes(B, max_blocks)
+    if n == 0:
+        raise SmlaError("smla_span_scores_workspace_bytes: invalid sizes")
+    return int(n)
+
+
+def span_scores(q, keys, block_table, seq_lens, sm_scale, scores=None, workspace=None, wait_timeout_ns: int = 0,
+                debug_flags: int = 0, stream=None):
+    """smla_span_scores: fp32 [B,4 max_blocks], the attention each span of a request should get
+    by its key, summed over the heads.  Without a ``workspace`` one is allocated for the call
+    (and its error word is lost)."""
+    dev = _device(q, "q")
+    B = q.shape[0] if q.dim() == 3 else -1
+    blocks = block_table.shape[1] if isinstance(block_table, torch.Tensor) and block_table.dim() == 2 else -1
+    if scores is None:
+        scores = _new(stream, (max(B, 0), max(blocks, 0) * PAGE_SPANS), torch.float32, dev)
+    x, k, t, l, s = _args(
+        dev, (q, torch.bfloat16, (B, HEADS, DIM), "q"), (keys, torch.bfloat16, (None, PAGE_SPANS, DIM), "keys"),
+        (block_table, torch.int32, (B, blocks), "block_table"), (seq_lens, torch.int32, (B,), "seq_lens"),
+        (scores, torch.float32, (B, blocks * PAGE_SPANS), "scores"))
+    if workspace is None:
+        workspace = _scratch(span_scores_workspace_bytes(B, blocks), dev, stream)
+    w, = _args(dev, (workspace, torch.uint8, None, "workspace"))
+    opts = None
+    if wait_timeout_ns or debug_flags:
+        opts = ctypes.byref(_Options(0, 0, wait_timeout_ns, debug_flags, 0))
+    rc = library().smla_span_scores(x, k, t, l, float(sm_scale), s, B, HEADS, blocks, keys.shape[0], w,
+                                    workspace.numel(), opts, _stream(stream))
+    _check(rc, "smla_span_scores")
+    return scores
 
 
 def select_spans(scores, seq_lens, nsel: int, keep_first: int = 0, keep_last: int = 0, spans=None, topk_idx=None,
@@ -358,9 +410,7 @@ def decode_spans(q, kv_cache, block_table, seq_lens, sm_scale, spans=None, out=N
         (spans, torch.int32, (B, nsel), "spans"), (out, torch.bfloat16, (B, HEADS, DIM), "out"),
         (lse, torch.float32, (B, HEADS), "lse"))
     if workspace is None:
-        workspace = _new(stream, decode_spans_workspace_bytes(B), torch.uint8, dev)
-        # only the error word has to start at zero
-        _zero_error_word(workspace, stream)
+        workspace = _scratch(decode_spans_workspace_bytes(B), dev, stream)
     w, = _args(dev, (workspace, torch.uint8, None, "workspace"))
     opts = None
     if wait_timeout_ns or debug_flags:
@@ -369,13 +419,3 @@ def decode_spans(q, kv_cache, block_table, seq_lens, sm_scale, spans=None, out=N
                                      kv_cache.shape[0], w, workspace.numel(), opts, _stream(stream))
     _check(rc, "smla_decode_spans")
     return out, lse
-
-
-def _zero_error_word(workspace, stream) -> None:
-    if stream is None:
-        workspace[:4].zero_()
-        return
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_stream(stream), device=workspace.device)
-    with torch.cuda.stream(stream):
-        workspace[:4].zero_()

@@ -36,6 +36,7 @@
 
 #include "smla_device.cuh"
 #include "smla_host.cuh"
+#include "smla_range.cuh"
 #include "smla_tile.cuh"
 
 namespace smla {
@@ -164,67 +165,6 @@ __device__ __forceinline__ long long tiles_of(const Params &p, int b) {
     if (p.spans) return (p.nsel + 1) / 2;
     const long long n = min(static_cast<long long>(len), static_cast<long long>(p.max_blocks) * kPageTokens);
     return (n + kTile - 1) / kTile;
-}
-
-// The CTA's range of tiles [begin, end) and where it begins.
-struct Range {
-    long long begin, end, per;
-    int b;               // request of tile `begin`
-    long long at;        // its first tile's index inside that request
-};
-
-// Every thread of the CTA.  The tile counts are scanned over the block; CTA 0 leaves the
-// prefix sums for the join kernel.
-__device__ __forceinline__ Range find_range(const Params &p, int tid) {
-    const int lane = tid & 31, warp = tid >> 5;
-    const int each = (p.B + kThreads - 1) / kThreads;
-    const int b0 = min(p.B, tid * each), b1 = min(p.B, b0 + each);
-    long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += tiles_of(p, b);
-    long long incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-    }
-    long long *scan = sm_scan();
-    if (lane == 31) scan[warp] = incl;
-    __syncthreads();
-    long long before = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-        const long long v = scan[w];
-        if (w < warp) before += v;
-        total += v;
-    }
-    before += incl - mine;
-    Range r;
-    r.per = max(1ll, (total + gridDim.x - 1) / gridDim.x);
-    r.begin = min(total, r.per * blockIdx.x);
-    r.end = min(total, r.begin + r.per);
-    if (before <= r.begin && r.begin < before + mine) {
-        long long at = before;
-        int b = b0;
-        for (;; ++b) {
-            const long long n = tiles_of(p, b);
-            if (r.begin < at + n) break;
-            at += n;
-        }
-        scan[kThreads / 32] = b;
-        scan[kThreads / 32 + 1] = r.begin - at;
-    }
-    if (blockIdx.x == 0) {
-        long long at = before;
-        for (int b = b0; b < b1; ++b) {
-            p.prefix[b] = at;
-            at += tiles_of(p, b);
-        }
-        if (tid == 0) p.prefix[p.B] = total;
-    }
-    __syncthreads();
-    r.b = r.begin < r.end ? static_cast<int>(scan[kThreads / 32]) : p.B;
-    r.at = r.begin < r.end ? scan[kThreads / 32 + 1] : 0;
-    return r;
 }
 
 // ------------------------------------------------------------------ the walk
@@ -809,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The tiles need a 1024-byte aligned base (128-byte swizzle); the base is the same for every
     // CTA of a launch.
     const bool misplaced = (smem_addr(g_smem) & 1023u) != 0;
-    const Range range = find_range(p, tid);
+    const Range range = find_range<kThreads>([&](int b) { return tiles_of(p, b); }, p.B, sm_scan(), p.prefix);
     if (misplaced || range.begin >= range.end) {  // nothing to do, or the join writes NaN
         if (tid == 0) {
             p.failed[blockIdx.x] = misplaced ? 1 : 0;

@@ -21,6 +21,7 @@ def lib():
 READ = [A, A, A, 5, A, 2, 3, 4, A, 1, A, None]
 KEYS = [A, A, A, A, A, 5, 2, 3, 4, A, A, None]
 DECODE = [A, A, A, None, 0, A, 0.1, A, A, 2, 64, 3, 4, A, 1 << 30, None, None]
+SCORES = [A, A, A, A, 0.1, A, 2, 64, 3, 4, A, 1 << 30, None, None]
 SELECT = [A, 100, A, 8, 1, 1, A, A, 2, None]
 
 
@@ -60,6 +61,18 @@ def test_decode_spans_refuses(lib):
     assert lib.smla_decode_spans_workspace_bytes(0) == 0 and lib.smla_decode_spans_workspace_bytes(65536) == 0
 
 
+def test_span_scores_refuses(lib):
+    _refused(lib.smla_span_scores, SCORES, [(k, None) for k in (0, 1, 2, 3, 5, 10)] + [(4, float("nan")), (6, 0), (6, 65536),
+             (7, 32), (8, 0), (8, (1 << 23) + 1), (9, 0), (9, 1 << 23), (0, ODD16), (1, ODD16), (10, A + 128), (2, ODD),
+             (3, ODD), (5, ODD), (11, 1000)])
+    for nsplit, out_bf16 in ((2, 0), (0, 1)):
+        opts = smla.binding._Options(nsplit, out_bf16, 0, 0, 0)
+        _refused(lib.smla_span_scores, SCORES, [(12, ctypes.byref(opts))])
+    assert lib.smla_span_scores_workspace_bytes(0, 5) == 0 and lib.smla_span_scores_workspace_bytes(5, 0) == 0
+    # header, 2 tiles of 64 (maximum, sum) per request, 64 fp32 per span
+    assert lib.smla_span_scores_workspace_bytes(3, 40) == 256 + 3 * 2 * 64 * 8 + 3 * 160 * 64 * 4
+
+
 def test_binding_refuses_host_tensors():
     i = torch.zeros(3, dtype=torch.int32)
     with pytest.raises(smla.SmlaError):
@@ -74,7 +87,7 @@ def test_binding_refuses_host_tensors():
 def test_entry_points_take_their_argument_counts(lib):
     # every argument is described to ctypes: a call with one missing raises instead of running
     for fn, args in ((lib.smla_read_kv, READ), (lib.smla_span_keys, KEYS), (lib.smla_select_spans, SELECT),
-                     (lib.smla_decode_spans, DECODE)):
+                     (lib.smla_decode_spans, DECODE), (lib.smla_span_scores, SCORES)):
         assert len(fn.argtypes) == len(args)
         with pytest.raises((TypeError, ctypes.ArgumentError)):
             fn(*args[:-1])
