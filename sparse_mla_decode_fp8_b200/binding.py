@@ -48,6 +48,8 @@ _lib = None
 def library():
     """Load libsmla.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(_build.LIB):
@@ -229,83 +231,102 @@ def write_kv(latents, req, pos, block_table, kv_cache, err=None, stream=None) ->
 
 
 # ---------------------------------------------------------------- long contexts: spans and reading back
-def _args(device, *tensors):
-    """Device pointers of (tensor, dtype, shape, name) entries, which must be dense CUDA
-    tensors of that dtype and shape (None entries of a shape are free) on ``device``, the
-    current one: the library launches on the current device."""
-    if device.type != "cuda" or device.index != torch.cuda.current_device():
-        raise SmlaError(f"tensors must be on the current CUDA device, got {device}")
-    ptrs = []
-    for t, dtype, shape, name in tensors:
-        if t is None:
-            ptrs.append(None)
-            continue
-        p = _dev(t, dtype, name)
-        if t.device != device:
-            raise SmlaError(f"{name} is on {t.device}, others on {device}")
-        if shape is not None and (t.dim() != len(shape) or any(a is not None and a != b for a, b in zip(shape, t.shape))):
-            raise SmlaError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-        ptrs.append(p)
-    return ptrs
+# These calls take a few microseconds of GPU time at small sizes, so what the binding checks it checks
+# cheaply: one comparison of dtype, device index, shape and density per tensor.
+_U8, _I32, _U32, _F32, _BF16 = torch.uint8, torch.int32, torch.uint32, torch.float32, torch.bfloat16
 
 
-def _device(t, name) -> torch.device:
+def _current(t, name) -> int:
+    """The device index of ``t``, which must be the current CUDA device: the library launches there."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise SmlaError(f"{name} must be a CUDA tensor")
-    return t.device
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
+        raise SmlaError(f"{name} must be on the current CUDA device, got {t.device}")
+    return dev
 
 
-def _as_stream(stream, device) -> torch.cuda.Stream:
+def _ptr(t, dtype, dev: int, shape, name) -> int:
+    """Device pointer of a dense tensor of this dtype, device and shape (None: any size there)."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+            got = t.shape
+            if got == shape or (len(got) == len(shape) and all(a is None or a == b for a, b in zip(shape, got))):
+                return t.data_ptr()
+    except AttributeError:
+        pass
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise SmlaError(f"{name} must be a CUDA tensor")
+    raise SmlaError(f"{name} must be a contiguous {dtype} {list(shape)} on device {dev}, got {t.dtype} {list(t.shape)} on {t.device}")
+
+
+def _raw_stream(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
+def _size(t, dims: int, name) -> torch.Size:
+    if not isinstance(t, torch.Tensor) or t.dim() != dims:
+        raise SmlaError(f"{name} must be a tensor of {dims} dimensions")
+    return t.shape
+
+
+def _as_stream(stream, dev: int) -> torch.cuda.Stream:
     if isinstance(stream, torch.cuda.Stream):
         return stream
-    return torch.cuda.ExternalStream(_stream(stream), device=device)
+    return torch.cuda.ExternalStream(_stream(stream), device=dev)
 
 
-def _new(stream, shape, dtype, device, zero=False) -> torch.Tensor:
+def _new(stream, shape, dtype, dev: int) -> torch.Tensor:
     """A tensor allocated on the stream that will write it."""
-    make = torch.zeros if zero else torch.empty
     if stream is None:
-        return make(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(_as_stream(stream, device)):
-        return make(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
+    with torch.cuda.stream(_as_stream(stream, dev)):
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
 
 
-def _scratch(nbytes: int, device, stream) -> torch.Tensor:
+def _scratch(nbytes: int, dev: int, stream) -> torch.Tensor:
     """A workspace for one call: only the error word has to start at zero."""
-    ws = _new(stream, nbytes, torch.uint8, device)
+    ws = _new(stream, nbytes, _U8, dev)
     if stream is None:
         ws[:4].zero_()
     else:
-        with torch.cuda.stream(_as_stream(stream, device)):
+        with torch.cuda.stream(_as_stream(stream, dev)):
             ws[:4].zero_()
     return ws
 
 
-def _err(err, device):
+def _workspace(ws, dev: int) -> int:
+    if not isinstance(ws, torch.Tensor) or ws.dtype is not _U8 or ws.get_device() != dev or not ws.is_contiguous():
+        raise SmlaError(f"workspace must be a contiguous uint8 tensor on device {dev}")
+    return ws.data_ptr()
+
+
+def _err(err, dev: int):
     if err is None:
         return None
-    if not isinstance(err, torch.Tensor) or err.dtype not in (torch.int32, torch.uint32) or err.numel() < 1:
+    if not isinstance(err, torch.Tensor) or err.dtype not in (_I32, _U32) or err.numel() < 1 or err.get_device() != dev:
         raise SmlaError("err must be a CUDA int32/uint32 tensor")
-    return _args(device, (err, err.dtype, None, "err"))[0]
+    return err.data_ptr()
 
 
 def read_kv(kv_cache, req, pos, block_table, out=None, out_dtype=None, err=None, stream=None):
     """smla_read_kv: the cached tokens at position pos[i] of request req[i] as latents [n,512],
     bf16 (the default) or fp32; rows of tokens out of range are zeros, and ``err`` receives
     SMLA_FLAG_BAD_PAGE."""
-    dev = _device(kv_cache, "kv_cache")
+    dev = _current(kv_cache, "kv_cache")
     if out_dtype is None:
-        out_dtype = out.dtype if out is not None else torch.bfloat16
-    if out_dtype not in (torch.float32, torch.bfloat16):
+        out_dtype = out.dtype if out is not None else _BF16
+    if out_dtype is not _F32 and out_dtype is not _BF16:
         raise SmlaError("out must be float32 or bfloat16")
-    n = req.shape[0] if isinstance(req, torch.Tensor) and req.dim() == 1 else -1
-    if out is None and n >= 0:
+    (n,) = _size(req, 1, "req")
+    B, blocks = _size(block_table, 2, "block_table")
+    pages = _size(kv_cache, 2, "kv_cache")[0]
+    if out is None:
         out = _new(stream, (n, DIM), out_dtype, dev)
-    c, r, p, t, o = _args(dev, (kv_cache, torch.uint8, (None, PAGE_BYTES), "kv_cache"), (req, torch.int32, (None,), "req"),
-                          (pos, torch.int32, (n,), "pos"), (block_table, torch.int32, (None, None), "block_table"),
-                          (out, out_dtype, (n, DIM), "out"))
-    rc = library().smla_read_kv(c, r, p, n, t, block_table.shape[0], block_table.shape[1], kv_cache.shape[0], o,
-                                1 if out_dtype == torch.bfloat16 else 0, _err(err, dev), _stream(stream))
+    rc = library().smla_read_kv(
+        _ptr(kv_cache, _U8, dev, (pages, PAGE_BYTES), "kv_cache"), _ptr(req, _I32, dev, (n,), "req"),
+        _ptr(pos, _I32, dev, (n,), "pos"), n, _ptr(block_table, _I32, dev, (B, blocks), "block_table"), B, blocks, pages,
+        _ptr(out, out_dtype, dev, (n, DIM), "out"), 1 if out_dtype is _BF16 else 0, _err(err, dev), _raw_stream(stream, dev))
     _check(rc, "smla_read_kv")
     return out
 
@@ -314,15 +335,15 @@ def span_keys(kv_cache, block_table, seq_lens, req, span, keys, err=None, stream
     """smla_span_keys: recomputes the keys of span[i] of request req[i] in ``keys``
     (bf16 [num_pages,4,512], returned); ``err`` receives SMLA_FLAG_BAD_PAGE when a span is
     skipped."""
-    dev = _device(kv_cache, "kv_cache")
-    pages = kv_cache.shape[0]
-    n = req.shape[0] if isinstance(req, torch.Tensor) and req.dim() == 1 else -1
-    B, blocks = block_table.shape if isinstance(block_table, torch.Tensor) and block_table.dim() == 2 else (-1, -1)
-    c, t, l, r, s, k = _args(dev, (kv_cache, torch.uint8, (None, PAGE_BYTES), "kv_cache"),
-                             (block_table, torch.int32, (None, None), "block_table"),
-                             (seq_lens, torch.int32, (B,), "seq_lens"), (req, torch.int32, (None,), "req"),
-                             (span, torch.int32, (n,), "span"), (keys, torch.bfloat16, (pages, PAGE_SPANS, DIM), "keys"))
-    rc = library().smla_span_keys(c, t, l, r, s, n, B, blocks, pages, k, _err(err, dev), _stream(stream))
+    dev = _current(kv_cache, "kv_cache")
+    (n,) = _size(req, 1, "req")
+    B, blocks = _size(block_table, 2, "block_table")
+    pages = _size(kv_cache, 2, "kv_cache")[0]
+    rc = library().smla_span_keys(
+        _ptr(kv_cache, _U8, dev, (pages, PAGE_BYTES), "kv_cache"), _ptr(block_table, _I32, dev, (B, blocks), "block_table"),
+        _ptr(seq_lens, _I32, dev, (B,), "seq_lens"), _ptr(req, _I32, dev, (n,), "req"), _ptr(span, _I32, dev, (n,), "span"),
+        n, B, blocks, pages, _ptr(keys, _BF16, dev, (pages, PAGE_SPANS, DIM), "keys"), _err(err, dev),
+        _raw_stream(stream, dev))
     _check(rc, "smla_span_keys")
     return keys
 
@@ -339,23 +360,21 @@ def span_scores(q, keys, block_table, seq_lens, sm_scale, scores=None, workspace
     """smla_span_scores: fp32 [B,4 max_blocks], the attention each span of a request should get
     by its key, summed over the heads.  Without a ``workspace`` one is allocated for the call
     (and its error word is lost)."""
-    dev = _device(q, "q")
-    B = q.shape[0] if q.dim() == 3 else -1
-    blocks = block_table.shape[1] if isinstance(block_table, torch.Tensor) and block_table.dim() == 2 else -1
+    dev = _current(q, "q")
+    B, blocks = _size(block_table, 2, "block_table")
+    pages = _size(keys, 3, "keys")[0]
     if scores is None:
-        scores = _new(stream, (max(B, 0), max(blocks, 0) * PAGE_SPANS), torch.float32, dev)
-    x, k, t, l, s = _args(
-        dev, (q, torch.bfloat16, (B, HEADS, DIM), "q"), (keys, torch.bfloat16, (None, PAGE_SPANS, DIM), "keys"),
-        (block_table, torch.int32, (B, blocks), "block_table"), (seq_lens, torch.int32, (B,), "seq_lens"),
-        (scores, torch.float32, (B, blocks * PAGE_SPANS), "scores"))
+        scores = _new(stream, (B, blocks * PAGE_SPANS), _F32, dev)
     if workspace is None:
         workspace = _scratch(span_scores_workspace_bytes(B, blocks), dev, stream)
-    w, = _args(dev, (workspace, torch.uint8, None, "workspace"))
     opts = None
     if wait_timeout_ns or debug_flags:
         opts = ctypes.byref(_Options(0, 0, wait_timeout_ns, debug_flags, 0))
-    rc = library().smla_span_scores(x, k, t, l, float(sm_scale), s, B, HEADS, blocks, keys.shape[0], w,
-                                    workspace.numel(), opts, _stream(stream))
+    rc = library().smla_span_scores(
+        _ptr(q, _BF16, dev, (B, HEADS, DIM), "q"), _ptr(keys, _BF16, dev, (pages, PAGE_SPANS, DIM), "keys"),
+        _ptr(block_table, _I32, dev, (B, blocks), "block_table"), _ptr(seq_lens, _I32, dev, (B,), "seq_lens"), sm_scale,
+        _ptr(scores, _F32, dev, (B, blocks * PAGE_SPANS), "scores"), B, HEADS, blocks, pages, _workspace(workspace, dev),
+        workspace.numel(), opts, _raw_stream(stream, dev))
     _check(rc, "smla_span_scores")
     return scores
 
@@ -364,19 +383,18 @@ def select_spans(scores, seq_lens, nsel: int, keep_first: int = 0, keep_last: in
                  tokens: bool = True, stream=None):
     """smla_select_spans: (spans int32 [B,nsel], topk_idx int32 [B,64 nsel]), the second None
     when ``tokens`` is false."""
-    dev = _device(scores, "scores")
-    B, width = scores.shape if scores.dim() == 2 else (-1, -1)
-    nsel, keep_first, keep_last = int(nsel), int(keep_first), int(keep_last)
+    dev = _current(scores, "scores")
+    B, width = _size(scores, 2, "scores")
     if not 1 <= nsel <= MAX_NSEL:
         raise SmlaError(f"nsel must lie in [1, {MAX_NSEL}]")
     if spans is None:
-        spans = _new(stream, (max(B, 0), nsel), torch.int32, dev)
+        spans = _new(stream, (B, nsel), _I32, dev)
     if topk_idx is None and tokens:
-        topk_idx = _new(stream, (max(B, 0), nsel * SPAN_TOKENS), torch.int32, dev)
-    x, l, s, i = _args(dev, (scores, torch.float32, (None, None), "scores"), (seq_lens, torch.int32, (B,), "seq_lens"),
-                       (spans, torch.int32, (B, nsel), "spans"),
-                       (topk_idx, torch.int32, (B, nsel * SPAN_TOKENS), "topk_idx"))
-    rc = library().smla_select_spans(x, width, l, nsel, keep_first, keep_last, s, i, B, _stream(stream))
+        topk_idx = _new(stream, (B, nsel * SPAN_TOKENS), _I32, dev)
+    rc = library().smla_select_spans(
+        _ptr(scores, _F32, dev, (B, width), "scores"), width, _ptr(seq_lens, _I32, dev, (B,), "seq_lens"), nsel, keep_first,
+        keep_last, _ptr(spans, _I32, dev, (B, nsel), "spans"),
+        None if topk_idx is None else _ptr(topk_idx, _I32, dev, (B, nsel * SPAN_TOKENS), "topk_idx"), B, _raw_stream(stream, dev))
     _check(rc, "smla_select_spans")
     return spans, topk_idx
 
@@ -393,29 +411,28 @@ def decode_spans(q, kv_cache, block_table, seq_lens, sm_scale, spans=None, out=N
     """smla_decode_spans: (out bf16 [B,64,512], lse fp32 [B,64]) over the whole sequences, or
     over ``spans`` (int32 [B,nsel]) of them.  Without a ``workspace`` one is allocated for the
     call (and its error word is lost)."""
-    dev = _device(q, "q")
-    B = q.shape[0] if q.dim() == 3 else -1
-    nsel = 0
+    dev = _current(q, "q")
+    B, blocks = _size(block_table, 2, "block_table")
+    pages = _size(kv_cache, 2, "kv_cache")[0]
+    nsel, listed = 0, None
     if spans is not None:
-        nsel = spans.shape[1] if isinstance(spans, torch.Tensor) and spans.dim() == 2 else -1
+        nsel = _size(spans, 2, "spans")[1]
         if not 1 <= nsel <= MAX_NSEL:  # an empty list is not "every span"
             raise SmlaError(f"spans must be [B, nsel] with nsel in [1, {MAX_NSEL}]")
+        listed = _ptr(spans, _I32, dev, (B, nsel), "spans")
     if out is None:
-        out = _new(stream, (max(B, 0), HEADS, DIM), torch.bfloat16, dev)
+        out = _new(stream, (B, HEADS, DIM), _BF16, dev)
     if lse is None:
-        lse = _new(stream, (max(B, 0), HEADS), torch.float32, dev)
-    x, c, t, l, s, o, e = _args(
-        dev, (q, torch.bfloat16, (B, HEADS, DIM), "q"), (kv_cache, torch.uint8, (None, PAGE_BYTES), "kv_cache"),
-        (block_table, torch.int32, (B, None), "block_table"), (seq_lens, torch.int32, (B,), "seq_lens"),
-        (spans, torch.int32, (B, nsel), "spans"), (out, torch.bfloat16, (B, HEADS, DIM), "out"),
-        (lse, torch.float32, (B, HEADS), "lse"))
+        lse = _new(stream, (B, HEADS), _F32, dev)
     if workspace is None:
         workspace = _scratch(decode_spans_workspace_bytes(B), dev, stream)
-    w, = _args(dev, (workspace, torch.uint8, None, "workspace"))
     opts = None
     if wait_timeout_ns or debug_flags:
         opts = ctypes.byref(_Options(0, 1, wait_timeout_ns, debug_flags, 0))
-    rc = library().smla_decode_spans(x, c, t, s, nsel, l, float(sm_scale), o, e, B, HEADS, block_table.shape[1],
-                                     kv_cache.shape[0], w, workspace.numel(), opts, _stream(stream))
+    rc = library().smla_decode_spans(
+        _ptr(q, _BF16, dev, (B, HEADS, DIM), "q"), _ptr(kv_cache, _U8, dev, (pages, PAGE_BYTES), "kv_cache"),
+        _ptr(block_table, _I32, dev, (B, blocks), "block_table"), listed, nsel, _ptr(seq_lens, _I32, dev, (B,), "seq_lens"),
+        sm_scale, _ptr(out, _BF16, dev, (B, HEADS, DIM), "out"), _ptr(lse, _F32, dev, (B, HEADS), "lse"), B, HEADS, blocks,
+        pages, _workspace(workspace, dev), workspace.numel(), opts, _raw_stream(stream, dev))
     _check(rc, "smla_decode_spans")
     return out, lse
