@@ -265,7 +265,8 @@ int smla_read_kv(const uint8_t *kv_cache, const int32_t *req, const int32_t *pos
  *               request b at [block_table[b][j / 4]][j % 4] (written; the others are left)
  *   err         device uint32 or NULL: SMLA_FLAG_BAD_PAGE is or-ed in when a span is skipped
  *               (req outside [0, B), a span that holds no token of the request or lies behind
- *               max_blocks, a page outside [0, num_pages)); nothing is written for it
+ *               max_blocks, a page outside [0, num_pages)); nothing is written for it.
+ *               SMLA_FLAG_TIMEOUT: a copy did not arrive within a second; keys are NaN
  *   n >= 0 (0: nothing is launched).  A span may be listed twice.  One launch on `stream`.
  */
 int smla_span_keys(const uint8_t *kv_cache, const int32_t *block_table, const int32_t *seq_lens, const int32_t *req,

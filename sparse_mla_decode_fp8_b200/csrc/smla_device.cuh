@@ -129,19 +129,23 @@ __device__ __forceinline__ float ue8m0_value(uint32_t s) {
     return __uint_as_float(s == 0u ? 0x00400000u : s == 255u ? 0x7FC00000u : s << 23);
 }
 
-// Four e4m3 bytes times a scale -> four fp32 values (exact unless they leave fp32's range).
-__device__ __forceinline__ void e4m3x4_values(uint32_t four, float scale, float *x) {
+// Four e4m3 bytes -> four fp32 values.
+__device__ __forceinline__ void e4m3x4_values(uint32_t four, float *x) {
     uint32_t h[2];
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[0]) : "h"(static_cast<unsigned short>(four & 0xFFFFu)));
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[1]) : "h"(static_cast<unsigned short>(four >> 16)));
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
+    for (int k = 0; k < 2; ++k)
         asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
             : "=f"(x[2 * k]), "=f"(x[2 * k + 1])
             : "r"(h[k]));
-        x[2 * k] *= scale;
-        x[2 * k + 1] *= scale;
-    }
+}
+
+// The same times a scale (exact unless the products leave fp32's range).
+__device__ __forceinline__ void e4m3x4_values(uint32_t four, float scale, float *x) {
+    e4m3x4_values(four, x);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] *= scale;
 }
 
 }  // namespace smla
