@@ -112,6 +112,12 @@ __device__ __forceinline__ bool barrier_or(uint32_t id, uint32_t nthreads, bool 
     return out != 0;
 }
 
+// ---------------------------------------------------------------- kernels in a row
+// Lets a kernel launched behind this one be scheduled from now on.
+__device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// Waits until the kernel before this one in the stream is complete and its writes are visible.
+__device__ __forceinline__ void wait_for_prior_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---------------------------------------------------------------- clusters
 __device__ __forceinline__ uint32_t cluster_ctarank() {
     uint32_t r;

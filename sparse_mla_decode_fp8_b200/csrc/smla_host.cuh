@@ -73,5 +73,21 @@ inline int encode_q_map(CUtensorMap *map, const void *q, int B) {
     return r == CUDA_SUCCESS ? SMLA_OK : SMLA_ERR_INVALID;
 }
 
+// Launches a kernel that may be scheduled while the one before it in the stream still runs; it has to
+// call wait_for_prior_kernel() before it touches what that one writes.
+template <class Kernel, class... Args>
+cudaError_t launch_after(Kernel kernel, dim3 grid, unsigned threads, cudaStream_t stream, const Args &...args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 }  // namespace host
 }  // namespace smla

@@ -21,8 +21,10 @@ __device__ __forceinline__ Range find_range(Tiles tiles_of, int B, long long *sc
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int each = (B + kThreads - 1) / kThreads;
     const int b0 = min(B, tid * each), b1 = min(B, b0 + each);
-    long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += tiles_of(b);
+    // with one request a thread (B <= kThreads) its length is read once
+    const long long head = b0 < b1 ? tiles_of(b0) : 0;
+    long long mine = head;
+    for (int b = b0 + 1; b < b1; ++b) mine += tiles_of(b);
     long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -45,11 +47,7 @@ __device__ __forceinline__ Range find_range(Tiles tiles_of, int B, long long *sc
     if (before <= r.begin && r.begin < before + mine) {
         long long at = before;
         int b = b0;
-        for (;; ++b) {
-            const long long n = tiles_of(b);
-            if (r.begin < at + n) break;
-            at += n;
-        }
+        for (long long n = head; r.begin >= at + n; n = tiles_of(++b)) at += n;
         scan[kThreads / 32] = b;
         scan[kThreads / 32 + 1] = r.begin - at;
     }
@@ -57,7 +55,7 @@ __device__ __forceinline__ Range find_range(Tiles tiles_of, int B, long long *sc
         long long at = before;
         for (int b = b0; b < b1; ++b) {
             prefix[b] = at;
-            at += tiles_of(b);
+            if (b + 1 < b1) at += b == b0 ? head : tiles_of(b);
         }
         if (tid == 0) prefix[B] = total;
     }
