@@ -75,7 +75,8 @@ enum Bar : int {
     kBarRingFull = 0,               // + slot
     kBarRingEmpty = kRing,          // + slot: dequant warps, softmax warps and the MMA thread are done with it
     kBarQ = 2 * kRing,              // Q of the current request landed
-    kBarKvFull = kBarQ + 1,         // + dims chunk c: chunk written (4 warps)
+    kBarRope = kBarQ + 1,           // rope values of the tile landed
+    kBarKvFull = kBarRope + 1,         // + dims chunk c: chunk written (4 warps)
     kBarKvFree = kBarKvFull + 4,    // + c: the PV of chunk c is done
     kBarS = kBarKvFree + 4,         // S^T of the tile complete
     kBarP = kBarS + 1,              // P^T written (8 warps)
@@ -414,21 +415,22 @@ __device__ __forceinline__ void nope_role(const Params &p, uint32_t tmem, int c,
     }
 }
 
-// Dims chunk 3: the last nope group and the rope values, loaded once the tile before is stored.
-__device__ __forceinline__ void rope_role(const Params &p, int t, int lane) {
+// Dims chunk 3: the last nope group, loaded once the tile before is stored, and the rope values, which
+// TMA puts in place once the PV of the tile before has released them.  A box is a span's 64 rows:
+// those behind the span's count come along (they are inside the page) and are zeroed afterwards.
+// Returns the number of tiles whose rope values it has asked for.
+__device__ __forceinline__ uint32_t tail_role(const Params &p, const CUtensorMap *tmap_rope, int t, int lane) {
     const int own = own_row(t), h = half_of(t), sw = own & 7;
-    const uint32_t base = smem_addr(g_smem + kSmemKV) + 6 * (kTile * 128) + own * 128;
+    const uint32_t kb6 = smem_addr(g_smem + kSmemKV) + 6 * (kTile * 128);
     Source s;
-    if (!all_wait(kBarRingFull, 0, p) || sm_ring()[0].b < 0) return;
+    int code[2];
+    if (!all_wait(kBarRingFull, 0, p) || sm_ring()[0].b < 0) return 0;
     s = tile_source(p, 0);
+    code[0] = sm_ring()[0].code[0];
+    code[1] = sm_ring()[0].code[1];
     for (int k = 0;; ++k) {
-        Bytes32 raw[2], rope[4];
+        Bytes32 raw[2];
         uint32_t scale[2];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int tok = own + 32 * (j & 1);
-            rope[j] = load32(s.row[j >> 1] + tok * kRowBytes + kNope + 32 * (t & 3), tok < s.count[j >> 1]);
-        }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int tok = own + 32 * j;
@@ -436,28 +438,41 @@ __device__ __forceinline__ void rope_role(const Params &p, int t, int lane) {
             raw[j] = load32((h ? s.row[1] : s.row[0]) + tok * kRowBytes + 384 + 32 * (t & 1), valid);
             scale[j] = load_scale(s, h, tok, 6, valid);
         }
+        const int count[2] = {s.count[0], s.count[1]}, now[2] = {code[0], code[1]};
         __syncwarp();
         if (lane == 0) mbar_arrive(sm_bar(kBarRingEmpty + k % kRing));
         // the next tile's pages: what its loads need is in registers before this tile is stored
-        if (!all_wait(kBarRingFull + (k + 1) % kRing, ((k + 1) / kRing) & 1, p)) return;
-        const bool more = sm_ring()[(k + 1) % kRing].b >= 0;
+        if (!all_wait(kBarRingFull + (k + 1) % kRing, ((k + 1) / kRing) & 1, p)) return k;
+        const Tile &next = sm_ring()[(k + 1) % kRing];
+        const bool more = next.b >= 0;
         s = tile_source(p, (k + 1) % kRing);
+        code[0] = next.code[0];
+        code[1] = next.code[1];
         uint4 v[2][4];
 #pragma unroll
         for (int j = 0; j < 2; ++j) convert_nope(raw[j], scale[j], v[j]);
-        if (k > 0 && !all_wait(kBarKvFree + 3, (k - 1) & 1, p)) return;
+        if (k > 0 && !all_wait(kBarKvFree + 3, (k - 1) & 1, p)) return k;
+        if (t == 0) {
+            mbar_arrive_expect_tx(sm_bar(kBarRope), ((now[0] >= 0 ? 1u : 0u) + (now[1] >= 0 ? 1u : 0u)) * kSpan * 128u);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) store_nope(base + (64 * h + 32 * j) * 128, t & 1, sw, v[j]);
+            for (int u = 0; u < 2; ++u)
+                if (now[u] >= 0)
+                    tma_load_3d(g_smem + kSmemKV + 7 * (kTile * 128) + u * (kSpan * 128), tmap_rope, kNope,
+                                (now[u] & 3) * kSpan, now[u] >> 2, sm_bar(kBarRope));
+        }
+        __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t first = base + kTile * 128 + 32 * 128 * j + (((2 * (t & 3)) ^ sw) << 4);
-            sts_v4(first, rope[j].a);
-            sts_v4(first ^ 16, rope[j].b);
+        for (int j = 0; j < 2; ++j) store_nope(kb6 + (64 * h + 32 * j + own) * 128, t & 1, sw, v[j]);
+        if (count[0] < kSpan || count[1] < kSpan) {  // uniform over the warpgroup
+            if (!all_wait(kBarRope, k & 1, p)) return k + 1;
+            if ((t & 63) >= ((t >> 6) ? count[1] : count[0]))
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sts_v4(kb6 + kTile * 128 + t * 128 + 16 * i, make_uint4(0u, 0u, 0u, 0u));
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(sm_bar(kBarKvFull + 3));
-        if (!more) return;
+        if (!more) return k + 1;
     }
 }
 
@@ -507,7 +522,7 @@ __device__ __forceinline__ void mma_role(const Params &p, const CUtensorMap *tma
         // MMAs that are queued by then
 #pragma unroll
         for (int c = 0; c < 4; c += 2) {
-            ok = all_wait(kBarKvFull + c, par, p) && all_wait(kBarKvFull + c + 1, par, p);
+            ok = all_wait(kBarKvFull + c, par, p) && all_wait(kBarKvFull + c + 1, par, p) && (c == 0 || all_wait(kBarRope, par, p));
             if (!ok) break;
             tc_fence_after_sync();
             if (leader) {
@@ -744,7 +759,8 @@ __device__ __forceinline__ void fewer_registers() {
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
-    span_decode_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tmap_q) {
+    span_decode_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tmap_q,
+                       const __grid_constant__ CUtensorMap tmap_rope) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // The tiles need a 1024-byte aligned base (128-byte swizzle); the base is the same for every
     // CTA of a launch.
@@ -767,6 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(sm_bar(kBarRingEmpty + i), kDequantWarps + kSoftmaxWarps + 1);
         }
         mbar_init(sm_bar(kBarQ), 1);
+        mbar_init(sm_bar(kBarRope), 1);
         for (int c = 0; c < 4; ++c) {
             mbar_init(sm_bar(kBarKvFull + c), kDequantWarps / kChunks);
             mbar_init(sm_bar(kBarKvFree + c), 1);
@@ -789,7 +806,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             nope_role(p, tmem, warp >> 2, tid & 127, warp & 3, lane);
         } else {
             more_registers<kRegsRope>();
-            rope_role(p, tid & 127, lane);
+            const uint32_t copies = tail_role(p, &tmap_rope, tid & 127, lane);
+            if (tid == 32 * (kDequantWarps - 4) && copies)  // the last copy asked for
+                (void)mbar_wait(sm_bar(kBarRope), (copies - 1) & 1, p.timeout_ns);
+            __syncwarp();
         }
     } else if (warp < kMmaWarp) {
         softmax_role(p, tmem, warp & 3, (warp - kDequantWarps) >> 2, lane);
@@ -890,6 +910,22 @@ Layout layout_for(int B, int grid) {
     return l;
 }
 
+// The cache as [num_pages][256][576] bytes; boxes of a span's 64 rows x 128 bytes.
+int encode_cache_map(CUtensorMap *map, const uint8_t *cache, int num_pages) {
+    PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    const int rc = smla::host::tensor_map_encoder(fn);
+    if (rc != SMLA_OK) return rc;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(smla::kRowBytes), static_cast<cuuint64_t>(smla::kPageTokens),
+                          static_cast<cuuint64_t>(num_pages)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(smla::kRowBytes), static_cast<cuuint64_t>(smla::kPageBytes)};
+    cuuint32_t box[3] = {128, kSpan, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t *>(cache), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? SMLA_OK : SMLA_ERR_INVALID;
+}
+
 int prepare_kernel(int dev) {
     static std::mutex mutex;
     static bool ready[smla::host::kMaxDevices] = {};
@@ -934,8 +970,9 @@ int smla_decode_spans(const void *q, const uint8_t *kv_cache, const int32_t *blo
     if (workspace_bytes < l.bytes) return SMLA_ERR_INVALID;
     rc = prepare_kernel(dev);
     if (rc != SMLA_OK) return rc;
-    alignas(64) CUtensorMap tmap_q;
+    alignas(64) CUtensorMap tmap_q, tmap_rope;
     rc = smla::host::encode_q_map(&tmap_q, q, B);
+    if (rc == SMLA_OK) rc = encode_cache_map(&tmap_rope, kv_cache, num_pages);
     if (rc != SMLA_OK) return rc;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     Params p{};
@@ -959,7 +996,7 @@ int smla_decode_spans(const void *q, const uint8_t *kv_cache, const int32_t *blo
     p.debug_flags = opts ? opts->debug_flags : 0u;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     (void)cudaGetLastError();
-    span_decode_kernel<<<static_cast<unsigned>(sms), kThreads, kSmemBytes, st>>>(p, tmap_q);
+    span_decode_kernel<<<static_cast<unsigned>(sms), kThreads, kSmemBytes, st>>>(p, tmap_q, tmap_rope);
     if (cudaGetLastError() != cudaSuccess) return SMLA_ERR_LAUNCH;
     join_kernel<<<static_cast<unsigned>(B) * (SMLA_HEADS / kJoinWarps), 32 * kJoinWarps, 0, st>>>(p, sms);
     return cudaGetLastError() == cudaSuccess ? SMLA_OK : SMLA_ERR_LAUNCH;
