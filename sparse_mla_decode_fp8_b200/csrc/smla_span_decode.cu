@@ -22,12 +22,14 @@
 // softmax and the epilogue; of the last, one warp issues the MMAs and one walks the CTA's range and
 // publishes a tile's pages in a ring.
 //
-// What bounds it (64 requests of 65536 tokens, 950 us: 2.6 TB/s, 580 TFLOP/s; a tile takes 7,700
+// What bounds it (64 requests of 65536 tokens, 940 us: 2.6 TB/s, 585 TFLOP/s; a tile takes about 7,500
 // cycles): shared memory's port.  The MMAs of a tile read 128 bytes a cycle for 3,100 cycles, the
-// conversions store for 1,000, and the loads of the raw rows take the same pipe a cycle for 32 bytes,
-// 2,300: without them a tile takes 5,900.  They cannot come by TMA, since Q, the tile and P^T
-// leave no room for raw rows: tiles of 96 tokens that do leave it (and whose scores still take
-// MMAs of 128 rows) took 1,140 us, rope values alone by TMA with 16-byte loads of the rest 1,120.
+// conversions store for 1,000, and the loads of the raw nope rows take the same pipe a cycle for 32
+// bytes, 1,800 (timed without any row loads, a tile took 5,900).  They cannot all come by TMA,
+// since Q, the tile and P^T leave 13 KB: tiles of 96 tokens, which leave room for all raw rows and
+// whose scores still take MMAs of 128 rows, took 1,060 us; chunk 1 by TMA through the place of P^T
+// 1,090.  Rope values by TMA straight into the tile gain 3 %.  With few tokens a start of 15,000
+// cycles counts: cold instructions, the lookups, one tile's chain of loads and barriers.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -478,7 +480,8 @@ __device__ __forceinline__ uint32_t tail_role(const Params &p, const CUtensorMap
 
 // ------------------------------------------------------------------ MMA issue (one warp)
 // The warp walks its loop converged, so that descriptors stay in uniform registers, and one
-// elected lane issues.
+// elected lane issues: 50 cycles an MMA, 80 to 100 by one lane of divergent code.  Loops over the chunks
+// are unrolled (rolled ones: 7 % more time for the whole kernel).
 __device__ __forceinline__ void issue_pv(uint32_t d, uint32_t a_lo, uint32_t b_lo, bool accumulate) {
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks) {  // 16 tokens a step, 2 KB apart in the MN-major V^T and P^T
