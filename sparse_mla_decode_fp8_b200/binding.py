@@ -372,7 +372,7 @@ def span_scores(q, keys, block_table, seq_lens, sm_scale, scores=None, workspace
         opts = ctypes.byref(_Options(0, 0, wait_timeout_ns, debug_flags, 0))
     rc = library().smla_span_scores(
         _ptr(q, _BF16, dev, (B, HEADS, DIM), "q"), _ptr(keys, _BF16, dev, (pages, PAGE_SPANS, DIM), "keys"),
-        _ptr(block_table, _I32, dev, (B, blocks), "block_table"), _ptr(seq_lens, _I32, dev, (B,), "seq_lens"), sm_scale,
+        _ptr(block_table, _I32, dev, (B, blocks), "block_table"), _ptr(seq_lens, _I32, dev, (B,), "seq_lens"), float(sm_scale),
         _ptr(scores, _F32, dev, (B, blocks * PAGE_SPANS), "scores"), B, HEADS, blocks, pages, _workspace(workspace, dev),
         workspace.numel(), opts, _raw_stream(stream, dev))
     _check(rc, "smla_span_scores")
@@ -432,7 +432,7 @@ def decode_spans(q, kv_cache, block_table, seq_lens, sm_scale, spans=None, out=N
     rc = library().smla_decode_spans(
         _ptr(q, _BF16, dev, (B, HEADS, DIM), "q"), _ptr(kv_cache, _U8, dev, (pages, PAGE_BYTES), "kv_cache"),
         _ptr(block_table, _I32, dev, (B, blocks), "block_table"), listed, nsel, _ptr(seq_lens, _I32, dev, (B,), "seq_lens"),
-        sm_scale, _ptr(out, _BF16, dev, (B, HEADS, DIM), "out"), _ptr(lse, _F32, dev, (B, HEADS), "lse"), B, HEADS, blocks,
+        float(sm_scale), _ptr(out, _BF16, dev, (B, HEADS, DIM), "out"), _ptr(lse, _F32, dev, (B, HEADS), "lse"), B, HEADS, blocks,
         pages, _workspace(workspace, dev), workspace.numel(), opts, _raw_stream(stream, dev))
     _check(rc, "smla_decode_spans")
     return out, lse

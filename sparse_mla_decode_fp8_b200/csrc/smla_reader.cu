@@ -6,7 +6,8 @@
 // infinity), and so is the fp32 output.  The bf16 output is that product rounded once to
 // nearest even: it is exact too unless s < 10 (subnormal bf16) or the value leaves the range.
 //
-// HBM-bound: 584 bytes read and 1024 (bf16) or 2048 (fp32) written per token.  A warp takes
+// HBM-bound: 584 bytes read and 1024 (bf16) or 2048 (fp32) written per token; 120,000 tokens as fp32
+// (317 MB) take 54 us, 89 % of the measured copy bandwidth.  A warp takes
 // kReadTokens tokens at a time, so that the three dependent loads (request and position, block
 // table, row) of several tokens are in flight together.  A lane holds 8 (bf16) or 4 (fp32)
 // consecutive dims of each pass, so that every store of a warp is 512 contiguous bytes.

@@ -5,12 +5,16 @@
 // leaves x and, per 128 spans and head, their maximum m and sum l = sum_j 2^(x - m); the second
 // joins these to lambda_h = M + log2 sum l 2^(m - M) and sums 2^(x_hj - lambda_h) over the heads in a
 // fixed order.  All of it is fp32.  The second is launched while the first still runs and waits for it
-// (2 us a call less).
+// (2 us a call less); it reads what the first wrote through L2, not the read-only path, which holds only
+// for data older than the kernel.
 //
 // Work: 1,024 bytes and 65,536 flops per span, 64 flop/byte: bound by the keys' way through HBM.  One CTA
 // per SM walks an equal contiguous part of all requests' 128-span tiles (lengths are read on the
 // device) and keeps up to 7 of the 8 key chunks [128 spans x 64 dims] in flight; Q stays in
 // shared memory for the CTA's tiles of a request.  x (256 bytes a span) goes through L2.
+// 64 requests of 65,536 tokens take 31 us in a graph for a floor of 11 (67 MB of keys): start, lookups and the
+// first loads about 7, the keys 14, x written and read again and the second kernel's start 10.  Few
+// spans: 13 us, nearly all of it the chain start - load - MMA - statistics - second kernel.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -350,6 +354,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // sum over the heads, 16 lanes of 4 heads per span.
 __global__ void __launch_bounds__(kScoreThreads) span_scores_kernel(const __grid_constant__ Params p) {
     __shared__ float part_m[4][kHeads], part_l[4][kHeads], lambda[kHeads];
+    // Every block waits, also one that needs nothing: this kernel must not end before the first one.
+    wait_for_prior_kernel();
     const int t = threadIdx.x, b = blockIdx.y, first = blockIdx.x * kScoreSpans;
     const int spans = spans_of(p, b), tiles = (spans + kTile - 1) / kTile;
     float *scores = p.scores + static_cast<size_t>(b) * p.width;
@@ -357,12 +363,11 @@ __global__ void __launch_bounds__(kScoreThreads) span_scores_kernel(const __grid
         if (t < kScoreSpans && first + t < p.width) scores[first + t] = 0.0f;
         return;
     }
-    wait_for_prior_kernel();
     const int h = t & 63, part = t >> 6;
     float m = -INFINITY, l = 0.0f;
     bool bad = false;  // a tile whose CTA gave up
     for (int i = part; i < tiles; i += 4) {
-        const float2 s = __ldg(p.stats + (static_cast<size_t>(b) * p.tiles + i) * kHeads + h);
+        const float2 s = __ldcg(p.stats + (static_cast<size_t>(b) * p.tiles + i) * kHeads + h);
         bad |= isnan(s.y);
         const float up = fmaxf(m, s.x);
         if (up != -INFINITY) l = l * exp2f(m - up) + s.y * exp2f(s.x - up);
@@ -377,7 +382,8 @@ __global__ void __launch_bounds__(kScoreThreads) span_scores_kernel(const __grid
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             sum += up == -INFINITY ? part_l[i][t] : part_l[i][t] * exp2f(part_m[i][t] - up);
-        lambda[t] = up + log2f(sum);  // -inf where no span has a key
+        // no span has a key: every x is -inf, and 0 lets 2^(x - lambda) be 0
+        lambda[t] = up == -INFINITY && sum == 0.0f ? 0.0f : up + log2f(sum);
     }
     __syncthreads();
     const int lane = t & 31, g = lane & 15;
@@ -386,10 +392,8 @@ __global__ void __launch_bounds__(kScoreThreads) span_scores_kernel(const __grid
         const int j = first + i;
         float s = 0.0f;
         if (j < spans) {
-            const float4 x = __ldg(reinterpret_cast<const float4 *>(p.x + (static_cast<size_t>(b) * p.width + j) * kHeads) + g);
-            // a span without a key counts for nothing; NaN where a CTA gave up
-            s = x.x == -INFINITY && !isnan(lam.x) ? 0.0f
-                                 : (exp2f(x.x - lam.x) + exp2f(x.y - lam.y)) + (exp2f(x.z - lam.z) + exp2f(x.w - lam.w));
+            const float4 x = __ldcg(reinterpret_cast<const float4 *>(p.x + (static_cast<size_t>(b) * p.width + j) * kHeads) + g);
+            s = (exp2f(x.x - lam.x) + exp2f(x.y - lam.y)) + (exp2f(x.z - lam.z) + exp2f(x.w - lam.w));
         }
 #pragma unroll
         for (int o = 8; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);

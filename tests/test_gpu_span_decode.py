@@ -149,6 +149,8 @@ def test_equals_the_sparse_decode_over_the_same_tokens():
     out, lse = smla.decode_spans(U.dev_bf16(qb), *d, sl, SCALE, spans=spans)
     ref, ref_lse = smla.decode(U.dev_bf16(qb), *d, idx, sl, SCALE)
     assert (lse - ref_lse).abs().max() <= 1e-5 * (1 + ref_lse.abs().max())
+    # one side rounds its weights and its output to bf16, 2^-9 of each in the mean, the other to two bf16
+    # terms and fp32: 2^-9 sqrt(2) = 2.8e-3 of the norm, below 5e-3
     assert (out.double() - ref.double()).norm() <= 5e-3 * ref.double().norm()
 
 
@@ -218,3 +220,83 @@ def test_refusals():
             smla.decode_spans(*args, SCALE)
     with pytest.raises(smla.SmlaError):
         smla.decode_spans(q, c, t, sl, float("nan"))
+
+
+def test_single_tokens_come_back_exactly_for_every_code_and_scale_byte():
+    # 255 requests of one token each, q = 0: the weight is 1 and the result the token itself.  Group g of request s
+    # has scale byte (s + 37 g) mod 255, dims cycle through the e4m3 codes; at scale bytes above 246 through
+    # those below 2, so that every value lies in the bf16 range.
+    codes = np.array([c for c in range(256) if c & 0x7F != 0x7F], np.uint8)
+    small = np.array([c for c in range(256) if c & 0x7F < 0x40], np.uint8)
+    cache = np.full((255, W.PAGE_BYTES), 0xFF, np.uint8)
+    rows, scales = W.row_views(cache)
+    rng = np.random.default_rng(1)
+    s = (np.arange(255)[:, None] + 37 * np.arange(7)) % 255
+    scales[:, 0, :7] = s
+    for g in range(7):
+        at = 64 * g + np.arange(64) + 13 * np.arange(255)[:, None]
+        rows[:, 0, 64 * g:64 * g + 64] = np.where(s[:, g:g + 1] > 246, small[at % len(small)], codes[at % len(codes)])
+    rows[:, 0, 448:] = W.to_bf16_bits(rng.standard_normal((255, 64)).astype(np.float32)).view(np.uint8).reshape(255, 128)
+    table = np.arange(255, dtype=np.int32)[:, None]
+    ws = _workspace(255)
+    out, lse = smla.decode_spans(torch.zeros((255, 64, 512), dtype=torch.bfloat16, device="cuda"), U.dev(cache), U.dev(table),
+                                 U.dev(np.ones(255, np.int32)), SCALE, workspace=ws)
+    assert smla.read_error(ws) == 0
+    want = independent.token_latents(cache, np.arange(255), np.zeros(255, np.int64))
+    got = out.double().cpu().numpy()
+    assert (lse == 0).all() and np.array_equal(got[:, :1].repeat(64, 1), got)
+    exact = np.concatenate([np.repeat(s >= 10, 64, 1), np.ones((255, 64), bool)], 1)
+    assert np.array_equal(got[:, 0][exact], want[exact])
+    # below scale byte 10 only what lies under the least normal number may round, by less than that number
+    assert (np.abs(got[:, 0] - want) < 2.0 ** -126).all()
+
+
+def test_nan_scale_nan_query_and_their_neighbours():
+    # a 0xFF scale byte of one token makes its request NaN, a NaN in one head's query that head; nothing else changes
+    lens = [300, 200, 1000]
+    cache, table = U.paged(lens, seed=16)
+    qb = _queries(3, 16)
+    ref, ref_lse = smla.decode_spans(U.dev_bf16(qb), U.dev(cache), U.dev(table), U.dev(np.array(lens, np.int32)), SCALE)
+    W.row_views(cache)[1][table[0, 1], 5, 3] = 0xFF
+    qb[1, 7, 100] = 0x7FC0
+    out, lse = smla.decode_spans(U.dev_bf16(qb), U.dev(cache), U.dev(table), U.dev(np.array(lens, np.int32)), SCALE)
+    assert torch.isnan(out[0]).all() and torch.isnan(lse[0]).all()
+    assert torch.isnan(out[1, 7]).all() and torch.isnan(lse[1, 7])
+    keep = torch.arange(64, device="cuda") != 7
+    assert torch.equal(out[1, keep], ref[1, keep]) and torch.equal(lse[1, keep], ref_lse[1, keep])
+    assert torch.equal(out[2], ref[2]) and torch.equal(lse[2], ref_lse[2])
+
+
+def test_two_calls_at_once_with_a_workspace_each():
+    lens = [[3000, 500, 41], [20000]]
+    calls = []
+    for i, n in enumerate(lens):
+        cache, table = U.paged(n, seed=17 + i)
+        qb = _queries(len(n), 17 + i)
+        calls.append((U.dev_bf16(qb), U.dev(cache), U.dev(table), U.dev(np.array(n, np.int32)), SCALE))
+    want = [smla.decode_spans(*c) for c in calls]
+    torch.cuda.synchronize()
+    streams, spaces = [torch.cuda.Stream(), torch.cuda.Stream()], [_workspace(len(n)) for n in lens]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        for c, st, ws in zip(calls, streams, spaces):
+            got.append(smla.decode_spans(*c, workspace=ws, stream=st))
+    torch.cuda.synchronize()
+    for i, (o, l) in enumerate(got):
+        assert torch.equal(o, want[i % 2][0]) and torch.equal(l, want[i % 2][1])
+    assert smla.read_error(spaces[0]) == 0 and smla.read_error(spaces[1]) == 0
+
+
+def test_tensors_out_of_alignment_or_with_gaps_are_refused():
+    cache, table = U.paged([300], seed=19)
+    q, c, t = U.dev_bf16(_queries(1, 19)), U.dev(cache), U.dev(table)
+    sl = U.dev(np.array([300], np.int32))
+    shifted = torch.empty(64 * 512 + 4, dtype=torch.bfloat16, device="cuda")[4:].view(1, 64, 512)  # 8 bytes on
+    off16 = torch.zeros(c.numel() + 16, dtype=torch.uint8, device="cuda")[16:].view(c.shape)       # 32 bytes needed
+    gaps = torch.zeros((1, 64, 1024), dtype=torch.bfloat16, device="cuda")[:, :, ::2]
+    ws = torch.zeros(smla.decode_spans_workspace_bytes(1) + 16, dtype=torch.uint8, device="cuda")[16:]
+    for args, kw in (((shifted, c, t, sl), {}), ((q, off16, t, sl), {}), ((gaps, c, t, sl), {}), ((q, c, t, sl), dict(out=shifted)),
+                     ((q, c, t, sl), dict(workspace=ws)), ((q, c, t, sl), dict(out=gaps))):
+        with pytest.raises(smla.SmlaError):
+            smla.decode_spans(*args, SCALE, **kw)

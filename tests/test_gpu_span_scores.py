@@ -163,6 +163,51 @@ def test_refusals():
         smla.span_scores(q, k, t, l, float("inf"))
 
 
+def test_nan_in_a_query_or_a_key_stays_with_its_request():
+    lens = [9000, 500, 700]
+    q, keys, table = _case(lens, 10)
+    args = (U.dev(table), U.dev(np.array(lens, np.int32)), SCALE)
+    ref = smla.span_scores(U.dev_bf16(q), U.dev_bf16(keys), *args)
+    q[0, 3, 9] = 0x7FC0
+    keys[table[1, 0], 2, 17] = 0x7FC0
+    got = smla.span_scores(U.dev_bf16(q), U.dev_bf16(keys), *args)
+    for b in (0, 1):
+        n = -(-lens[b] // 64)
+        assert torch.isnan(got[b, :n]).all() and not got[b, n:].any()
+    assert torch.equal(got[2], ref[2])
+
+
+def test_empty_requests_alone_and_calls_back_to_back_on_one_workspace():
+    # nothing but empty requests, then work, then nothing again, without a wait between the calls
+    q, keys, table = _case([20000, 20000], 11)
+    a = [U.dev_bf16(q), U.dev_bf16(keys), U.dev(table)]
+    lens = [[0, -4], [20000, 1], [0, 0], [8200, 20000]]
+    ws = _workspace(2, table.shape[1])
+    sl = [U.dev(np.array(n, np.int32)) for n in lens]
+    got = [smla.span_scores(*a, x, SCALE, workspace=ws) for x in sl]
+    torch.cuda.synchronize()
+    for g, n in zip(got, lens):
+        _check(g, q, keys, table, n, SCALE)
+
+
+def test_two_calls_at_once_with_a_workspace_each():
+    calls = []
+    for seed, lens in ((12, [20000, 3000]), (13, [64] * 40)):
+        q, keys, table = _case(lens, seed)
+        calls.append((U.dev_bf16(q), U.dev_bf16(keys), U.dev(table), U.dev(np.array(lens, np.int32)), SCALE))
+    want = [smla.span_scores(*c) for c in calls]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    spaces = [_workspace(*c[2].shape) for c in calls]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        for c, st, ws in zip(calls, streams, spaces):
+            got.append(smla.span_scores(*c, workspace=ws, stream=st))
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert torch.equal(g, want[i % 2])
+
+
 # ---------------------------------------------------------------- the operators in a row
 def test_a_decode_step_over_selected_spans():
     # prefill by the writer, keys of every span, then three steps: write a token, its span's key, scores,
