@@ -189,8 +189,11 @@ __global__ void __launch_bounds__(kKeyThreads, kKeyBlocks) span_keys_kernel(cons
 // candidate separates exactly nsel keys.  Then one pass in index order writes the spans above
 // the key and the first of those equal to it.  Bound by its chain of barriers, over 4 bytes read per
 // span: in a graph 5.6 us for one row of 128 spans, 8.5 us for 256 rows of up to 2,048.
-// Up to 2,048 spans 256 threads hold 8 keys each, up to 8,192 1,024 threads; longer rows are read again
-// from L2 on every pass.
+// The block is the smallest that holds a row in registers, 8 or 16 keys a thread: fewer warps at a
+// barrier.  256 rows (in a graph) of 2,048 spans: 256 x 8 8.7 us, 256 x 16 11.8, 512 x 16 18.0, 1,024 x 16 35;
+// of 4,096: 256 x 16 12.7, 256 x 32 19.8, 512 x 16 19.0; of 8,192: 512 x 16 21.3, 256 x 32 24.2, 1,024 x 8 26.1,
+// held nowhere 81.  64 rows of 16,384: 1,024 x 16 22.7, held nowhere 79.  Longer rows are read again from
+// L2 on every pass: 154 us for 64 rows of 32,768 (1,024 x 32 spills registers).
 __device__ __forceinline__ uint32_t order_key(float x) {
     if (isnan(x)) x = -INFINITY;
     if (x == 0.0f) x = 0.0f;
@@ -375,8 +378,12 @@ int smla_select_spans(const float *scores, int width, const int32_t *seq_lens, i
     const unsigned blocks = static_cast<unsigned>(B);
     if (width <= 256 * 8)
         select_spans_kernel<256, 8><<<blocks, 256, 0, st>>>(p);
-    else if (width <= 1024 * 8)
-        select_spans_kernel<1024, 8><<<blocks, 1024, 0, st>>>(p);
+    else if (width <= 256 * 16)
+        select_spans_kernel<256, 16><<<blocks, 256, 0, st>>>(p);
+    else if (width <= 512 * 16)
+        select_spans_kernel<512, 16><<<blocks, 512, 0, st>>>(p);
+    else if (width <= 1024 * 16)
+        select_spans_kernel<1024, 16><<<blocks, 1024, 0, st>>>(p);
     else
         select_spans_kernel<1024, 0><<<blocks, 1024, 0, st>>>(p);
     return cudaGetLastError() == cudaSuccess ? SMLA_OK : SMLA_ERR_LAUNCH;

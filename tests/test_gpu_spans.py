@@ -173,6 +173,16 @@ def test_select_spans_equals_sorting(width, kind):
         assert np.array_equal(idx.cpu().numpy(), want_idx), (nsel, first, last)
 
 
+@pytest.mark.parametrize("width", [4096, 4097, 16384, 16385, 40000])
+def test_select_spans_of_long_rows(width):
+    for kind in ("random", "special"):
+        x, lens = _select_case(width, kind, seed=width)
+        for nsel, first, last in [(1, 0, 0), (33, 1, 2), (1024, 4, 3)]:
+            spans, idx = smla.select_spans(U.dev(x), U.dev(lens), nsel, keep_first=first, keep_last=last)
+            want_spans, want_idx = U.select(x, lens, nsel, first, last)
+            assert np.array_equal(spans.cpu().numpy(), want_spans) and np.array_equal(idx.cpu().numpy(), want_idx)
+
+
 def test_select_spans_without_tokens_and_into_given_tensors():
     x, lens = _select_case(100, "random", 1)
     spans = torch.full((len(lens), 7), 55, dtype=torch.int32, device="cuda")
