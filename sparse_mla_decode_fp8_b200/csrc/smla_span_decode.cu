@@ -58,6 +58,11 @@ static_assert(32 * ((kDequantWarps - 4) * kRegsNope + 4 * kRegsRope + kSoftmaxWa
                   kThreads * kRegsLaunch && kThreads * kRegsLaunch <= 65536,
               "the shares are drawn from what the block was launched with");
 constexpr int kRing = 4;                                 // tiles published ahead
+// The chunks' order in both products, two at a time in the first: chunk 3 first, since its rope values are
+// copied in when the second product of the tile before has released it.
+__device__ constexpr int chunk_at(int i) { return (i + 3) % kChunks; }
+__device__ constexpr int pair_of(int c) { return (c + 1) % kChunks / 2; }
+static_assert(chunk_at(0) == 3 && pair_of(chunk_at(1)) == 0 && pair_of(chunk_at(2)) == 1, "3, 0 and 1, 2");
 constexpr uint32_t kBarIdSoftmax = 1;                    // named barrier of the softmax warps
 constexpr float kRescaleThreshold = 64.0f;               // log2 units
 constexpr int kJoinWarps = 8;
@@ -71,15 +76,16 @@ constexpr int kSmemScales = kSmemRing + kRing * 32;  // [kRing][128] scale rows 
 constexpr int kSmemRed = kSmemScales + kRing * 1024;   // [4][64] f32: per-quadrant maxima or sums
 constexpr int kSmemHeadM = kSmemRed + 1024;        // [64] m per head
 constexpr int kSmemAlpha = kSmemHeadM + 256;       // [64] rescale factors; 1/L in the epilogue
-constexpr int kSmemScan = kSmemAlpha + 256;        // block scan of the tile counts (a row per warp), the range's start
+constexpr int kSmemNegM = kSmemAlpha + 256;        // [64] -m per head
+constexpr int kSmemScan = kSmemNegM + 256;        // block scan of the tile counts (a row per warp), the range's start
 constexpr int kSmemBars = kSmemScan + 8 * (kThreads / 32 + 2);
 enum Bar : int {
     kBarRingFull = 0,               // + slot
     kBarRingEmpty = kRing,          // + slot: dequant warps, softmax warps and the MMA thread are done with it
     kBarQ = 2 * kRing,              // Q of the current request landed
     kBarRope = kBarQ + 1,           // rope values of the tile landed
-    kBarKvFull = kBarRope + 1,         // + dims chunk c: chunk written (4 warps)
-    kBarKvFree = kBarKvFull + 4,    // + c: the PV of chunk c is done
+    kBarKvFull = kBarRope + 1,      // + i: the chunks of pair i written (8 warps)
+    kBarKvFree = kBarKvFull + 2,    // + c: the PV of chunk c is done
     kBarS = kBarKvFree + 4,         // S^T of the tile complete
     kBarP = kBarS + 1,              // P^T written (8 warps)
     kBarDrain = kBarP + 1,
@@ -135,6 +141,7 @@ __device__ __forceinline__ uint64_t *sm_bar(int i) { return reinterpret_cast<uin
 __device__ __forceinline__ Tile *sm_ring() { return reinterpret_cast<Tile *>(g_smem + kSmemRing); }
 __device__ __forceinline__ float *sm_red() { return reinterpret_cast<float *>(g_smem + kSmemRed); }
 __device__ __forceinline__ float *sm_head_m() { return reinterpret_cast<float *>(g_smem + kSmemHeadM); }
+__device__ __forceinline__ float *sm_neg_m() { return reinterpret_cast<float *>(g_smem + kSmemNegM); }
 __device__ __forceinline__ float *sm_alpha() { return reinterpret_cast<float *>(g_smem + kSmemAlpha); }
 __device__ __forceinline__ long long *sm_scan() { return reinterpret_cast<long long *>(g_smem + kSmemScan); }
 __device__ __forceinline__ volatile int *sm_abort() { return reinterpret_cast<volatile int *>(g_smem + kSmemAbort); }
@@ -411,7 +418,7 @@ __device__ __forceinline__ void nope_role(const Params &p, uint32_t tmem, int c,
         part.store(c, t, park);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(sm_bar(kBarKvFull + c));
+        if (lane == 0) mbar_arrive(sm_bar(kBarKvFull + pair_of(c)));
         if (!more) return;
         part.convert(park);
     }
@@ -473,7 +480,7 @@ __device__ __forceinline__ uint32_t tail_role(const Params &p, const CUtensorMap
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(sm_bar(kBarKvFull + 3));
+        if (lane == 0) mbar_arrive(sm_bar(kBarKvFull + pair_of(3)));
         if (!more) return k + 1;
     }
 }
@@ -524,14 +531,16 @@ __device__ __forceinline__ void mma_role(const Params &p, const CUtensorMap *tma
         // two chunks at a time: a look at a barrier takes hundreds of cycles while MMAs run, more than the
         // MMAs that are queued by then
 #pragma unroll
-        for (int c = 0; c < 4; c += 2) {
-            ok = all_wait(kBarKvFull + c, par, p) && all_wait(kBarKvFull + c + 1, par, p) && (c == 0 || all_wait(kBarRope, par, p));
+        for (int i = 0; i < kChunks; i += 2) {
+            ok = (i > 0 || all_wait(kBarRope, par, p)) && all_wait(kBarKvFull + i / 2, par, p);
             if (!ok) break;
             tc_fence_after_sync();
             if (leader) {
 #pragma unroll
-                for (int e = c; e < c + 2; ++e)
-                    issue_qk_chunk(tmem + kTmemS, qk_a + e * 2 * ((kTile * 128) >> 4), qk_b + e * 2 * (8192 >> 4), e == 0);
+                for (int j = i; j < i + 2; ++j) {
+                    const int e = chunk_at(j);
+                    issue_qk_chunk(tmem + kTmemS, qk_a + e * 2 * ((kTile * 128) >> 4), qk_b + e * 2 * (8192 >> 4), j == 0);
+                }
             }
             __syncwarp();
         }
@@ -557,7 +566,8 @@ __device__ __forceinline__ void mma_role(const Params &p, const CUtensorMap *tma
         if (!ok) break;
         tc_fence_after_sync();
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int i = 0; i < kChunks; ++i) {
+            const int c = chunk_at(i);
             if (leader) {
                 issue_pv(tmem + 64 * c, pv_a + c * 2 * ((kTile * 128) >> 4), pv_b, !(flags & kFirst));
                 mma_commit(sm_bar(kBarKvFree + c));
@@ -603,6 +613,7 @@ __device__ __forceinline__ void raise_max(const Params &p, uint32_t tmem_lane, i
         const float mn = fmaxf(mo, tm);
         sm_alpha()[t] = (mo == -INFINITY) ? 0.0f : exp2f(mo - mn);
         sm_head_m()[t] = mn;
+        sm_neg_m()[t] = -mn;
     }
     named_barrier_sync(kBarIdSoftmax, kSoftmaxThreads);
     if (first) return;  // nothing accumulated yet
@@ -668,6 +679,17 @@ __device__ __forceinline__ void write_out(const Params &p, uint32_t tmem_lane, i
     }
 }
 
+// (three inputs to a maximum and two products an instruction: 1 % of the kernel's time)
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// (a, b) = (a, b) * c + (x, y)
+__device__ __forceinline__ void fma2(float &a, float &b, float c, float x, float y) {
+    asm("{\n.reg .b64 u, v, w;\nmov.b64 u, {%0, %1};\nmov.b64 v, {%2, %2};\nmov.b64 w, {%3, %4};\nfma.rn.f32x2 u, u, v, w;\nmov.b64 {%0, %1}, u;\n}"
+        : "+f"(a), "+f"(b) : "f"(c), "f"(x), "f"(y));
+}
 // Scores of this warp's heads in log2 units less the references (-inf for a masked token) and
 // their maximum.
 __device__ __forceinline__ float load_scores(uint32_t lane_addr, int hf, float c, bool whole, bool valid,
@@ -676,11 +698,9 @@ __device__ __forceinline__ float load_scores(uint32_t lane_addr, int hf, float c
     tmem_wait_ld();
 #pragma unroll
     for (int g = 0; g < 8; ++g) {
-        const float4 m = reinterpret_cast<const float4 *>(sm_head_m() + 32 * hf)[g];
-        x[4 * g] = fmaf(x[4 * g], c, -m.x);
-        x[4 * g + 1] = fmaf(x[4 * g + 1], c, -m.y);
-        x[4 * g + 2] = fmaf(x[4 * g + 2], c, -m.z);
-        x[4 * g + 3] = fmaf(x[4 * g + 3], c, -m.w);
+        const float4 m = reinterpret_cast<const float4 *>(sm_neg_m() + 32 * hf)[g];
+        fma2(x[4 * g], x[4 * g + 1], c, m.x, m.y);
+        fma2(x[4 * g + 2], x[4 * g + 3], c, m.z, m.w);
     }
     if (!whole) {  // a tile with masked tokens: uniform over the warps
 #pragma unroll
@@ -688,8 +708,10 @@ __device__ __forceinline__ float load_scores(uint32_t lane_addr, int hf, float c
     }
     float top[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-    for (int h = 4; h < 32; ++h) top[h & 3] = fmaxf(top[h & 3], x[h]);
-    return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+    for (int h = 4; h < 28; h += 8)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top[i] = max3(top[i], x[h + 2 * i], x[h + 2 * i + 1]);
+    return max3(max3(top[0], top[1], x[28]), max3(top[2], top[3], x[29]), fmaxf(x[30], x[31]));
 }
 
 __device__ __forceinline__ void softmax_role(const Params &p, uint32_t tmem, int q, int hf, int lane) {
@@ -708,16 +730,22 @@ __device__ __forceinline__ void softmax_role(const Params &p, uint32_t tmem, int
         const bool valid = (r & 63) < ((r >> 6) ? tile.count[1] : tile.count[0]);
         ok = ok && !done && all_wait(kBarS, par, p);
         tc_fence_after_sync();
+        // the weights before the verdict on the references (3 % less time than after it): those of a tile that
+        // passes them are computed again
         float x[32];
+#pragma unroll
+        for (int h = 0; h < 32; ++h) x[h] = 0.0f;
         bool over = first || !ok;
         if (!over) over = load_scores(lane_addr, hf, p.scale_log2, whole, valid, x) > kRescaleThreshold;
+#pragma unroll
+        for (int h = 0; h < 32; ++h) x[h] = fast_exp2(x[h]);
         if (barrier_or(kBarIdSoftmax, kSoftmaxThreads, over)) {
             if (barrier_or(kBarIdSoftmax, kSoftmaxThreads, !ok)) return;
             raise_max(p, lane_addr, q, hf, lane, valid, first);
             (void)load_scores(lane_addr, hf, p.scale_log2, whole, valid, x);
-        }
 #pragma unroll
-        for (int h = 0; h < 32; ++h) x[h] = fast_exp2(x[h]);
+            for (int h = 0; h < 32; ++h) x[h] = fast_exp2(x[h]);
+        }
 #pragma unroll
         for (int g = 0; g < 4; ++g)
             sts_v4(prow + (((4 * hf + g) ^ (r & 7)) << 4),
@@ -742,7 +770,7 @@ __device__ __forceinline__ void softmax_role(const Params &p, uint32_t tmem, int
         }
         tmem_wait_st();
         if (tile.flags & kLast) {
-            ok = all_wait(kBarKvFree + 3, par, p);  // commits complete in order: every chunk of O^T is final
+            ok = all_wait(kBarKvFree + chunk_at(3), par, p);  // commits complete in order: every chunk of O^T is final
             if (barrier_or(kBarIdSoftmax, kSoftmaxThreads, !ok)) return;
             tc_fence_after_sync();
             finish_sums(p, lane_addr, q, hf, lane, tile.b, tile.part);
@@ -788,7 +816,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(sm_bar(kBarQ), 1);
         mbar_init(sm_bar(kBarRope), 1);
         for (int c = 0; c < 4; ++c) {
-            mbar_init(sm_bar(kBarKvFull + c), kDequantWarps / kChunks);
+            if (c < 2) mbar_init(sm_bar(kBarKvFull + c), kDequantWarps / 2);
             mbar_init(sm_bar(kBarKvFree + c), 1);
         }
         mbar_init(sm_bar(kBarS), 1);
