@@ -22,14 +22,18 @@
 // softmax and the epilogue; of the last, one warp issues the MMAs and one walks the CTA's range and
 // publishes a tile's pages in a ring.
 //
-// What bounds it (64 requests of 65536 tokens, 940 us: 2.6 TB/s, 585 TFLOP/s; a tile takes about 7,500
-// cycles): shared memory's port.  The MMAs of a tile read 128 bytes a cycle for 3,100 cycles, the
-// conversions store for 1,000, and the loads of the raw nope rows take the same pipe a cycle for 32
-// bytes, 1,800 (timed without any row loads, a tile took 5,900).  They cannot all come by TMA,
-// since Q, the tile and P^T leave 13 KB: tiles of 96 tokens, which leave room for all raw rows and
-// whose scores still take MMAs of 128 rows, took 1,060 us; chunk 1 by TMA through the place of P^T
-// 1,090.  Rope values by TMA straight into the tile gain 3 %.  With few tokens a start of 15,000
-// cycles counts: cold instructions, the lookups, one tile's chain of loads and barriers.
+// What bounds it (64 requests of 65536 tokens, 860 us: 2.85 TB/s, 640 TFLOP/s; a tile takes about 7,100
+// cycles): the chain of one tile.  Q, one converted tile and P^T fill shared memory, so a chunk is
+// stored when the second product of the tile before has released it.  By clock stamps, from the hand-over
+// of P^T: second product 1,950 cycles, the last chunk stored 1,000 later (the first pair's MMAs run by
+// then), scores complete 2,000 after that, weights handed over 1,700 after that.  Under the chain lies shared
+// memory's port: the MMAs read 128 bytes a cycle for 3,100 cycles, the conversions store for 1,000, and the
+// loads of raw nope rows take the same pipe a cycle for 32 bytes, 1,800 (without row loads a tile
+// took 5,900).  Tried and slower: 96-token tiles with all raw rows by TMA 13 %, chunk 1 by TMA through
+// the place of P^T 16 %, row loads held back until P^T is done 14 %; the last nope group by TMA through
+// 8 KB of its own gains nothing, rope values by TMA straight into the tile 3 %.  With few tokens a start
+// of 15,000 cycles counts: cold instructions, the lookups, one tile's chain of loads and barriers; and a
+// part's 128 KB, stored in 5,000 cycles and read again by the join.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -53,8 +57,8 @@ constexpr int kMmaWarp = kDequantWarps + kSoftmaxWarps;  // 24
 constexpr int kWalkWarp = kMmaWarp + 1;                  // 25
 constexpr int kThreads = 32 * (kDequantWarps + kSoftmaxWarps + 4);
 // Registers a thread: 72 at launch (896 threads); the control warps give to those that dequantise.
-constexpr int kRegsLaunch = 72, kRegsNope = 80, kRegsRope = 80, kRegsSoftmax = 72, kRegsControl = 40;
-static_assert(32 * ((kDequantWarps - 4) * kRegsNope + 4 * kRegsRope + kSoftmaxWarps * kRegsSoftmax + 4 * kRegsControl) <=
+constexpr int kRegsLaunch = 72, kRegsNope = 80, kRegsTail = 80, kRegsSoftmax = 72, kRegsControl = 40;
+static_assert(32 * ((kDequantWarps - 4) * kRegsNope + 4 * kRegsTail + kSoftmaxWarps * kRegsSoftmax + 4 * kRegsControl) <=
                   kThreads * kRegsLaunch && kThreads * kRegsLaunch <= 65536,
               "the shares are drawn from what the block was launched with");
 constexpr int kRing = 4;                                 // tiles published ahead
@@ -270,18 +274,17 @@ __device__ __forceinline__ void walk(const Params &p, const Range &r, int lane) 
 
 // ------------------------------------------------------------------ dequantisation
 // Warpgroup c writes dims [128c, 128c + 128) of every tile: of c = 0..2 two nope groups, of c = 3
-// the last nope group and the rope values.  Thread t (0..127) of it works on the token rows
-// own + 32 j (j = 0..3, the first two in the first span) and the 32 bytes u = t & 3 of the chunk's
-// 128; for c = 3 on rope bytes 32 u.. of those rows and on 32 nope bytes of the two rows in span
-// h = u >> 1.
+// the last nope group, and it has the rope values copied in.  Thread t (0..127) of it works on the token
+// rows own + 32 j (j = 0..3, the first two in the first span) and the 32 bytes u = t & 3 of the chunk's
+// 128; for c = 3 on 32 nope bytes of the two rows in span h = u >> 1.
 //
 // own: a store phase is 8 lanes with 16 bytes each; the four lanes of a row would hit each
 // bank group twice (u and u + 2 write the same columns of two K-blocks), as would the next row's.
 // Lanes with h = 1 therefore take the row of the other parity, and the second four lanes a
-// row that differs in bits 0 and 1: 8 bank groups of the swizzled tile, for nope and rope.
+// row that differs in bits 0 and 1: 8 bank groups of the swizzled tile.
 //
-// One chunk per warpgroup and not all four in turn: a warp that converts chunk c + 1 with loads for
-// chunk c just issued was measured to wait for those (12,500 cycles a tile).
+// One chunk per warpgroup and not all four in turn: a warp that converts a chunk with loads for the
+// next just issued was measured to wait for those (12,500 cycles a tile).
 struct Source {
     const uint8_t *row[2];  // first token row of each span
     uint32_t scales;        // shared memory: the spans' scale rows, 512 bytes each
@@ -528,8 +531,8 @@ __device__ __forceinline__ void mma_role(const Params &p, const CUtensorMap *tma
             if (!ok) break;
             q_pending = false;
         }
-        // two chunks at a time: a look at a barrier takes hundreds of cycles while MMAs run, more than the
-        // MMAs that are queued by then
+        // two chunks at a time, with one barrier for both: a look at a barrier takes hundreds of cycles while
+        // MMAs run, more than the MMAs that are queued by then (single chunks, or 1 + 2 + 1: 4 % slower)
 #pragma unroll
         for (int i = 0; i < kChunks; i += 2) {
             ok = (i > 0 || all_wait(kBarRope, par, p)) && all_wait(kBarKvFull + i / 2, par, p);
@@ -836,7 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             more_registers<kRegsNope>();
             nope_role(p, tmem, warp >> 2, tid & 127, warp & 3, lane);
         } else {
-            more_registers<kRegsRope>();
+            more_registers<kRegsTail>();
             const uint32_t copies = tail_role(p, &tmap_rope, tid & 127, lane);
             if (tid == 32 * (kDequantWarps - 4) && copies)  // the last copy asked for
                 (void)mbar_wait(sm_bar(kBarRope), (copies - 1) & 1, p.timeout_ns);
