@@ -12,9 +12,10 @@
 // per SM walks an equal contiguous part of all requests' 128-span tiles (lengths are read on the
 // device) and keeps up to 7 of the 8 key chunks [128 spans x 64 dims] in flight; Q stays in
 // shared memory for the CTA's tiles of a request.  x (256 bytes a span) goes through L2.
-// 64 requests of 65,536 tokens take 31 us in a graph for a floor of 11 (67 MB of keys): start, lookups and the
-// first loads about 7, the keys 14, x written and read again and the second kernel's start 10.  Few
-// spans: 13 us, nearly all of it the chain start - load - MMA - statistics - second kernel.
+// 64 requests of 65,536 tokens take 28.7 us in a graph for a floor of 11 (67 MB of keys): besides HBM the
+// load-store pipe counts, a cycle for 32 bytes of keys and of x (x by 16-byte stores, half a sector
+// each: 30.8 us), and the chain start - load - MMA - statistics - second kernel, which is nearly all of the
+// 11 to 13 us that few spans take.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -272,8 +273,7 @@ __device__ __forceinline__ void stat_role(const Params &p, const Range &r, uint3
             for (int h = 0; h < 32; ++h) y[h] = x[h] = valid ? x[h] * p.scale_log2 : -INFINITY;
             if (j < c.spans)
 #pragma unroll
-                for (int g = 0; g < 8; ++g)
-                    reinterpret_cast<float4 *>(out + 32 * half)[g] = make_float4(x[4 * g], x[4 * g + 1], x[4 * g + 2], x[4 * g + 3]);
+                for (int g = 0; g < 4; ++g) st_global_v8(out + 32 * half + 8 * g, x + 8 * g);
             red[q * 64 + 32 * half + lane] = warp_transpose_reduce<true, 32>(y, lane);
         }
         named_barrier_sync(kBarIdStat, kStatThreads);
