@@ -334,10 +334,11 @@ struct Bytes32 {
 };
 __device__ __forceinline__ Bytes32 ld_stream_v8(const void *p) {
     Bytes32 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(v.a.x), "=r"(v.a.y), "=r"(v.a.z), "=r"(v.a.w), "=r"(v.b.x), "=r"(v.b.y), "=r"(v.b.z),
                    "=r"(v.b.w)
-                 : "l"(p));
+                 : "l"(p)
+                 : "memory");
     return v;
 }
 // 32 bytes, a whole sector (32-byte aligned).

@@ -73,13 +73,15 @@ inline int encode_q_map(CUtensorMap *map, const void *q, int B) {
     return r == CUDA_SUCCESS ? SMLA_OK : SMLA_ERR_INVALID;
 }
 
-// Launches a kernel that may be scheduled while the one before it in the stream still runs; it has to
-// call wait_for_prior_kernel() before it touches what that one writes.
+// Launches a kernel that may be scheduled while the one before it in the stream drains, or still runs if that
+// one allows it.  Every block of it has to call wait_for_prior_kernel(), before it touches memory
+// that an earlier kernel writes or reads.
 template <class Kernel, class... Args>
-cudaError_t launch_after(Kernel kernel, dim3 grid, unsigned threads, cudaStream_t stream, const Args &...args) {
+cudaError_t launch_after(Kernel kernel, dim3 grid, unsigned threads, size_t smem, cudaStream_t stream, const Args &...args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -174,7 +174,7 @@ __device__ __forceinline__ bool all_wait(int bar, uint32_t parity, const Params 
 
 // Number of tiles of request b.
 __device__ __forceinline__ long long tiles_of(const Params &p, int b) {
-    const int len = __ldg(p.seq_lens + b);
+    const int len = p.seq_lens[b];
     if (len <= 0) return 0;
     if (p.spans) return (p.nsel + 1) / 2;
     const long long n = min(static_cast<long long>(len), static_cast<long long>(p.max_blocks) * kPageTokens);
@@ -190,10 +190,10 @@ __device__ __forceinline__ void span_code(const Params &p, int b, int len, long 
     long long j = slot;
     if (p.spans) {
         if (slot >= p.nsel) return;
-        j = __ldg(p.spans + static_cast<size_t>(b) * p.nsel + slot);
+        j = p.spans[static_cast<size_t>(b) * p.nsel + slot];
     }
     if (j < 0 || j * kSpan >= len || j / (kPageTokens / kSpan) >= p.max_blocks) return;
-    const int page = __ldg(p.block_table + static_cast<size_t>(b) * p.max_blocks + j / (kPageTokens / kSpan));
+    const int page = p.block_table[static_cast<size_t>(b) * p.max_blocks + j / (kPageTokens / kSpan)];
     if (page < 0 || page >= p.num_pages) {
         atomicOr(p.err, SMLA_FLAG_BAD_PAGE);
         return;
@@ -216,7 +216,7 @@ __device__ __forceinline__ void walk(const Params &p, const Range &r, int lane) 
     int k = 0;  // tiles published
     for (int b = r.b; left > 0; ++b, at = 0) {
         const long long total = tiles_of(p, b);
-        const int len = __ldg(p.seq_lens + b);
+        const int len = p.seq_lens[b];
         const long long n = min(left, total - at);  // tiles of this segment
         if (n <= 0) continue;
         left -= n;
@@ -795,6 +795,9 @@ __device__ __forceinline__ void fewer_registers() {
 __global__ void __launch_bounds__(kThreads, 1)
     span_decode_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tmap_q,
                        const __grid_constant__ CUtensorMap tmap_rope) {
+    // Launched while the kernel before it drains (2 us a call).  No load in here is of the read-only kind, which
+    // holds only for data older than the kernel's launch.
+    wait_for_prior_kernel();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // The tiles need a 1024-byte aligned base (128-byte swizzle); the base is the same for every
     // CTA of a launch.
@@ -868,6 +871,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // a request without tiles, NaN where a CTA gave up, nothing for a request that one CTA wrote
 // whole, and otherwise the parts, in the order of the CTAs, with weights 2^(lambda - max).
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ Params p, int grid) {
+    wait_for_prior_kernel();
     const int b = blockIdx.x / (kHeads / kJoinWarps);
     const int h = blockIdx.x % (kHeads / kJoinWarps) * kJoinWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     const long long begin = p.prefix[b], n = p.prefix[b + 1] - begin, total = p.prefix[p.B];
@@ -1030,9 +1034,12 @@ int smla_decode_spans(const void *q, const uint8_t *kv_cache, const int32_t *blo
     p.debug_flags = opts ? opts->debug_flags : 0u;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     (void)cudaGetLastError();
-    span_decode_kernel<<<static_cast<unsigned>(sms), kThreads, kSmemBytes, st>>>(p, tmap_q, tmap_rope);
-    if (cudaGetLastError() != cudaSuccess) return SMLA_ERR_LAUNCH;
-    join_kernel<<<static_cast<unsigned>(B) * (SMLA_HEADS / kJoinWarps), 32 * kJoinWarps, 0, st>>>(p, sms);
+    if (smla::host::launch_after(span_decode_kernel, dim3(static_cast<unsigned>(sms)), kThreads, kSmemBytes, st, p, tmap_q, tmap_rope) !=
+        cudaSuccess)
+        return SMLA_ERR_LAUNCH;
+    // launched while the first kernel drains: 2 to 3 us a call
+    const dim3 grid(static_cast<unsigned>(B) * (SMLA_HEADS / kJoinWarps));
+    if (smla::host::launch_after(join_kernel, grid, 32 * kJoinWarps, 0, st, p, sms) != cudaSuccess) return SMLA_ERR_LAUNCH;
     return cudaGetLastError() == cudaSuccess ? SMLA_OK : SMLA_ERR_LAUNCH;
 }
 

@@ -5,17 +5,16 @@
 // leaves x and, per 128 spans and head, their maximum m and sum l = sum_j 2^(x - m); the second
 // joins these to lambda_h = M + log2 sum l 2^(m - M) and sums 2^(x_hj - lambda_h) over the heads in a
 // fixed order.  All of it is fp32.  The second is launched while the first still runs and waits for it
-// (2 us a call less); it reads what the first wrote through L2, not the read-only path, which holds only
-// for data older than the kernel.
+// (2 us a call less); it reads what the first wrote through L2.
 //
 // Work: 1,024 bytes and 65,536 flops per span, 64 flop/byte: bound by the keys' way through HBM.  One CTA
 // per SM walks an equal contiguous part of all requests' 128-span tiles (lengths are read on the
 // device) and keeps up to 7 of the 8 key chunks [128 spans x 64 dims] in flight; Q stays in
 // shared memory for the CTA's tiles of a request.  x (256 bytes a span) goes through L2.
-// 64 requests of 65,536 tokens take 28.7 us in a graph for a floor of 11 (67 MB of keys): besides HBM the
+// 64 requests of 65,536 tokens take 28.3 us in a graph for a floor of 11 (67 MB of keys): besides HBM the
 // load-store pipe counts, a cycle for 32 bytes of keys and of x (x by 16-byte stores, half a sector
 // each: 30.8 us), and the chain start - load - MMA - statistics - second kernel, which is nearly all of the
-// 11 to 13 us that few spans take.
+// 10 to 12.6 us that few spans take.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -105,7 +104,7 @@ __device__ __forceinline__ bool all_wait(int bar, uint32_t parity, const Params 
 }
 
 __device__ __forceinline__ int spans_of(const Params &p, int b) {
-    const int len = __ldg(p.seq_lens + b);
+    const int len = p.seq_lens[b];
     return len <= 0 ? 0 : static_cast<int>(min(static_cast<long long>(p.width), (static_cast<long long>(len) + kSpan - 1) / kSpan));
 }
 
@@ -149,7 +148,7 @@ __device__ __forceinline__ void load_role(const Params &p, const Range &r, int t
         const int j = c.tile * kTile + t;
         int code = -1;
         if (j < c.spans) {
-            const int page = __ldg(p.block_table + static_cast<size_t>(c.b) * p.max_blocks + j / kPageSpans);
+            const int page = p.block_table[static_cast<size_t>(c.b) * p.max_blocks + j / kPageSpans];
             if (page >= 0 && page < p.num_pages)
                 code = page * kPageSpans + j % kPageSpans;
             else
@@ -252,7 +251,7 @@ __device__ __forceinline__ void stat_role(const Params &p, const Range &r, uint3
         const int j = c.tile * kTile + t;
         bool valid = false;
         if (j < c.spans) {
-            const int page = __ldg(p.block_table + static_cast<size_t>(c.b) * p.max_blocks + j / kPageSpans);
+            const int page = p.block_table[static_cast<size_t>(c.b) * p.max_blocks + j / kPageSpans];
             valid = page >= 0 && page < p.num_pages;
         }
         ok = ok && all_wait(kBarS + buf, (n >> 1) & 1, p);
@@ -302,6 +301,9 @@ __device__ __forceinline__ void stat_role(const Params &p, const Range &r, uint3
 __global__ void __launch_bounds__(kThreads, 1)
     span_logits_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tmap_q) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // Launched while the kernel before it drains (1.5 us a call).  No load in here is of the read-only kind, which
+    // holds only for data older than the kernel's launch.
+    wait_for_prior_kernel();
     let_next_kernel_start();
     const Range range = find_range<kThreads>(
         [&](int b) { return static_cast<long long>((spans_of(p, b) + kTile - 1) / kTile); }, p.B,
@@ -485,10 +487,10 @@ int smla_span_scores(const void *q, const void *keys, const int32_t *block_table
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     (void)cudaGetLastError();
     const long long most = static_cast<long long>(B) * p.tiles;
-    span_logits_kernel<<<static_cast<unsigned>(most < sms ? most : sms), kThreads, kSmemBytes, st>>>(p, tmap_q);
-    if (cudaGetLastError() != cudaSuccess) return SMLA_ERR_LAUNCH;
+    const dim3 ctas(static_cast<unsigned>(most < sms ? most : sms));
+    if (smla::host::launch_after(span_logits_kernel, ctas, kThreads, kSmemBytes, st, p, tmap_q) != cudaSuccess) return SMLA_ERR_LAUNCH;
     const dim3 grid(static_cast<unsigned>((p.width + kScoreSpans - 1) / kScoreSpans), static_cast<unsigned>(B));
-    if (smla::host::launch_after(span_scores_kernel, grid, kScoreThreads, st, p) != cudaSuccess) return SMLA_ERR_LAUNCH;
+    if (smla::host::launch_after(span_scores_kernel, grid, kScoreThreads, 0, st, p) != cudaSuccess) return SMLA_ERR_LAUNCH;
     return cudaGetLastError() == cudaSuccess ? SMLA_OK : SMLA_ERR_LAUNCH;
 }
 

@@ -208,6 +208,41 @@ def test_two_calls_at_once_with_a_workspace_each():
         assert torch.equal(g, want[i % 2])
 
 
+def test_inputs_rewritten_right_before_each_call():
+    # lengths, queries, cache rows and keys change on the stream between the calls, with and without waits for the GPU:
+    # the calls start while the kernels before them drain, and must not see what those have yet to write
+    rng = np.random.default_rng(14)
+    table = U.dev(rng.permutation(40).reshape(2, 20).astype(np.int32))
+    base = torch.randn((2, 64, 512), device="cuda", generator=torch.Generator("cuda").manual_seed(2))
+    rows = torch.randn((30, 2, 512), device="cuda", generator=torch.Generator("cuda").manual_seed(3))
+    r = U.dev(np.arange(2, dtype=np.int32))
+    ws, ws2 = _workspace(2, 20), torch.zeros(smla.decode_spans_workspace_bytes(2), dtype=torch.uint8, device="cuda")
+
+    def steps(wait):
+        cache = torch.zeros((40, W.PAGE_BYTES), dtype=torch.uint8, device="cuda")
+        keys = torch.zeros((40, 4, 512), dtype=torch.bfloat16, device="cuda")
+        lens, q, got = U.dev(np.array([100, 3000], np.int32)), torch.empty((2, 64, 512), dtype=torch.bfloat16, device="cuda"), []
+        for i in range(30):
+            lens.add_(1)
+            q.copy_(base * (1 + i))
+            smla.write_kv(rows[i], r, lens - 1, table, cache)
+            smla.span_keys(cache, table, lens, r, (lens - 1) // 64, keys)
+            scores = smla.span_scores(q, keys, table, lens, SCALE, workspace=ws)
+            spans, _ = smla.select_spans(scores, lens, 5, keep_last=1)
+            out, lse = smla.decode_spans(q, cache, table, lens, SCALE, spans=spans, workspace=ws2)
+            whole = smla.decode_spans(q, cache, table, lens, SCALE, workspace=ws2)
+            got.append((scores, spans, out, lse, *whole))
+            lens.mul_(1)
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return got
+
+    for x, y in zip(steps(True), steps(False)):
+        for a, b in zip(x, y):
+            assert torch.equal(a, b)
+
+
 # ---------------------------------------------------------------- the operators in a row
 def test_a_decode_step_over_selected_spans():
     # prefill by the writer, keys of every span, then three steps: write a token, its span's key, scores,
