@@ -285,8 +285,9 @@ __device__ __forceinline__ void stat_role(const Params &p, const Range &r, uint3
             tmem_wait_ld();
 #pragma unroll
             for (int h = 0; h < 32; ++h) {
-                const float m = top[32 * half + h];
-                x[h] = valid && m != -INFINITY ? fast_exp2(x[h] * p.scale_log2 - m) : 0.0f;
+                const float s = valid ? x[h] * p.scale_log2 : -INFINITY;
+                // the test is on the score: the maximum (which passes NaN over) may be -inf beside a NaN
+                x[h] = s == -INFINITY ? 0.0f : fast_exp2(s - top[32 * half + h]);
             }
             red[q * 64 + 32 * half + lane] = warp_transpose_reduce<false, 32>(x, lane);
         }

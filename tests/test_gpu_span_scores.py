@@ -282,3 +282,33 @@ def test_a_decode_step_over_selected_spans():
         qv = independent.q_values(qb)
         U.check_decode(out, lse, qv, host, table, [want_idx[b][want_idx[b] >= 0] for b in range(B)], SCALE)
         U.check_decode(sparse, sparse_lse, qv, host, table, [want_idx[b][want_idx[b] >= 0] for b in range(B)], SCALE)
+
+
+@pytest.mark.parametrize("spans", [127, 128, 129, 130, 192, 256, 257])
+def test_a_nan_in_the_newest_key_reaches_every_span(spans):
+    # alone in its tile or not, the NaN is in the sum of every head
+    lens = [64 * spans - 63, 500]
+    q, keys, table = _case(lens, 15)
+    args = (U.dev(table), U.dev(np.array(lens, np.int32)), SCALE)
+    ref = smla.span_scores(U.dev_bf16(q), U.dev_bf16(keys), *args)
+    keys[table[0, (spans - 1) // 4], (spans - 1) % 4, 100] = 0x7FC0
+    got = smla.span_scores(U.dev_bf16(q), U.dev_bf16(keys), *args)
+    assert torch.isnan(got[0, :spans]).all() and not got[0, spans:].any()
+    assert torch.equal(got[1], ref[1])
+
+
+def test_keys_of_infinite_size():
+    # scores of -inf beside others weigh nothing, alone in a tile or not; a request that has no others has no weight
+    lens = [64 * 129, 64 * 20, 64 * 130]
+    q, keys, table = _case(lens, 17)
+    q[:, :, 9] = W.to_bf16_bits(np.ones(1, np.float32))
+    low = W.to_bf16_bits(np.array([-np.inf], np.float32))[0]
+    keys[table[0, 32], 0, 9] = low                     # span 128 of the first request
+    keys[table[1, 1], 2, 9] = low                      # span 6 of the second
+    for j in range(130):
+        keys[table[2, j // 4], j % 4, 9] = low         # all of the third
+    got = smla.span_scores(U.dev_bf16(q), U.dev_bf16(keys), U.dev(table), U.dev(np.array(lens, np.int32)), SCALE)
+    assert got[0, 128] == 0 and got[1, 6] == 0
+    for b, n in ((0, 129), (1, 20)):
+        assert not torch.isnan(got[b]).any() and abs(float(got[b, :n].double().sum()) - 64) <= 1e-4
+    assert not got[2].any()
