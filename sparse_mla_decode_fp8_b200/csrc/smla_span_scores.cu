@@ -400,7 +400,14 @@ __global__ void __launch_bounds__(kScoreThreads) span_scores_kernel(const __grid
         }
 #pragma unroll
         for (int o = 8; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (g == 0 && j < p.width) scores[j] = s;
+        if (g == 0 && j < p.width) {
+            // a request with a NaN: its spans in bad pages still score 0 (x = -inf, less a lambda of NaN)
+            if (isnan(s)) {
+                const int page = p.block_table[static_cast<size_t>(b) * p.max_blocks + j / kPageSpans];
+                if (page < 0 || page >= p.num_pages) s = 0.0f;
+            }
+            scores[j] = s;
+        }
     }
 }
 

@@ -312,3 +312,17 @@ def test_keys_of_infinite_size():
     for b, n in ((0, 129), (1, 20)):
         assert not torch.isnan(got[b]).any() and abs(float(got[b, :n].double().sum()) - 64) <= 1e-4
     assert not got[2].any()
+
+
+def test_a_nan_between_bad_pages():
+    # the NaN keys are the only ones of their tile; spans in bad pages score 0 whatever the others do
+    lens = [64 * 256, 64 * 40]
+    q, keys, table = _case(lens, 16)
+    keys[table[0, 32], :, 5] = 0x7FC0
+    table[0, 33:64] = -1
+    table[1, 3] = len(keys)
+    ws = _workspace(2, table.shape[1])
+    got = smla.span_scores(U.dev_bf16(q), U.dev_bf16(keys), U.dev(table), U.dev(np.array(lens, np.int32)), SCALE, workspace=ws)
+    assert smla.read_error(ws) == smla.SMLA_FLAG_BAD_PAGE
+    assert torch.isnan(got[0, :132]).all() and not got[0, 132:].any()
+    assert not torch.isnan(got[1]).any() and not got[1, 12:16].any()
