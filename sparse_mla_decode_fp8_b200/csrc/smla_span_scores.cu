@@ -358,10 +358,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 __global__ void __launch_bounds__(kScoreThreads) span_scores_kernel(const __grid_constant__ Params p) {
     __shared__ float part_m[4][kHeads], part_l[4][kHeads], lambda[kHeads];
     const int t = threadIdx.x, b = blockIdx.y, first = blockIdx.x * kScoreSpans;
+    // Every block waits, also one that needs nothing (this kernel must not end before the first one), and before it reads
+    // the lengths, which a kernel ahead of both may have written.
+    wait_for_prior_kernel();
     const int spans = spans_of(p, b), tiles = (spans + kTile - 1) / kTile;
     float *scores = p.scores + static_cast<size_t>(b) * p.width;
-    // Every block waits, also one that needs nothing: this kernel must not end before the first one.
-    wait_for_prior_kernel();
     if (first >= spans) {  // block-uniform: behind the sequence
         if (t < kScoreSpans && first + t < p.width) scores[first + t] = 0.0f;
         return;

@@ -326,3 +326,48 @@ def test_a_nan_between_bad_pages():
     assert smla.read_error(ws) == smla.SMLA_FLAG_BAD_PAGE
     assert torch.isnan(got[0, :132]).all() and not got[0, 132:].any()
     assert not torch.isnan(got[1]).any() and not got[1, 12:16].any()
+
+
+def test_calls_in_a_row_equal_calls_apart():
+    # the steps above against a run that waits for the GPU before every single call: no kernel can start there before
+    # what it reads is written
+    rng = np.random.default_rng(18)
+    table = U.dev(rng.permutation(600).reshape(2, 300).astype(np.int32))
+    base = torch.randn((2, 64, 512), device="cuda", generator=torch.Generator("cuda").manual_seed(8))
+    fill = torch.randn((600, 4, 512), device="cuda", generator=torch.Generator("cuda").manual_seed(9)).to(torch.bfloat16)
+    steps = [np.array(x, np.int32) for x in ([76000, 100], [0, 0], [64, 76800], [9000, 9000], [1, 0], [40000, 76800], [0, 1], [8193, 64])]
+    steps = [U.dev(x) for x in steps] * 3
+    ws, ws2 = _workspace(2, 300), torch.zeros(smla.decode_spans_workspace_bytes(2), dtype=torch.uint8, device="cuda")
+    cache = torch.zeros((600, W.PAGE_BYTES), dtype=torch.uint8, device="cuda")
+    rows = torch.randn((153600, 512), device="cuda", generator=torch.Generator("cuda").manual_seed(10))
+    at = torch.arange(153600, dtype=torch.int32, device="cuda")
+    smla.write_kv(rows, at // 76800, at % 76800, table, cache)
+
+    def run(apart):
+        def gap():
+            if apart:
+                torch.cuda.synchronize()
+        lens, q, keys, got = torch.zeros(2, dtype=torch.int32, device="cuda"), torch.empty_like(base, dtype=torch.bfloat16), fill.clone(), []
+        for i, new in enumerate(steps):
+            q.copy_(base * (1 + i))
+            keys.copy_(fill * (1 + i % 3))
+            lens.copy_(new)
+            gap()
+            scores = smla.span_scores(q, keys, table, lens, SCALE, workspace=ws)
+            gap()
+            lens.zero_()          # right behind the call: it has read its lengths by then
+            lens.copy_(new)
+            gap()
+            spans, _ = smla.select_spans(scores, lens, 9, keep_last=1)
+            gap()
+            out, lse = smla.decode_spans(q, cache, table, lens, SCALE, spans=spans, workspace=ws2)
+            gap()
+            lens.fill_(3)
+            gap()
+            got.append((scores, spans, out, lse))
+        torch.cuda.synchronize()
+        return got
+
+    for x, y in zip(run(True), run(False)):
+        for a, b in zip(x, y):
+            assert torch.equal(a, b)
