@@ -331,7 +331,8 @@ int smla_select_spans(const float *scores, int width, const int32_t *seq_lens, i
  *   kv_cache    32-byte aligned here
  *   opts        NULL, or options with nsplit 0 and out_bf16 1 (wait_timeout_ns, debug_flags)
  *   The other arguments are those of smla_decode.  A sequence longer than 256 max_blocks is
- *   cut there.  A request without tokens gets out = 0, lse = -inf; tokens in a page outside
+ *   cut there.  A request without tokens gets out = 0, lse = -inf; a token whose score is -inf
+ *   weighs 0, a head that has no other gets lse = -inf; tokens in a page outside
  *   [0, num_pages) count for nothing and set SMLA_FLAG_BAD_PAGE.  A wait that ran out makes the
  *   rows of the requests it touched NaN and sets SMLA_FLAG_TIMEOUT.
  * Two launches on `stream`: the work of all requests is cut into equal parts over the SMs by

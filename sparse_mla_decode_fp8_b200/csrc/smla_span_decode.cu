@@ -37,6 +37,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 
@@ -616,7 +617,8 @@ __device__ __forceinline__ void raise_max(const Params &p, uint32_t tmem_lane, i
         const float mn = fmaxf(mo, tm);
         sm_alpha()[t] = (mo == -INFINITY) ? 0.0f : exp2f(mo - mn);
         sm_head_m()[t] = mn;
-        sm_neg_m()[t] = -mn;
+        // no score above -inf yet: one that is -inf itself has to give 2^-inf and not 2^NaN, any other to raise m
+        sm_neg_m()[t] = mn == -INFINITY ? FLT_MAX : -mn;
     }
     named_barrier_sync(kBarIdSoftmax, kSoftmaxThreads);
     if (first) return;  // nothing accumulated yet

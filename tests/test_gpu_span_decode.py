@@ -300,3 +300,38 @@ def test_tensors_out_of_alignment_or_with_gaps_are_refused():
                      ((q, c, t, sl), dict(workspace=ws)), ((q, c, t, sl), dict(out=gaps))):
         with pytest.raises(smla.SmlaError):
             smla.decode_spans(*args, SCALE, **kw)
+
+
+def test_tokens_whose_scores_are_minus_infinity_weigh_nothing():
+    # the last token, alone in its tile (a part of its own), has -inf in one dim where the query is positive: its
+    # scores are -inf, its weight 0, and 0 times -inf makes that one dim of the output NaN, as the formula does
+    n = 257
+    cache, table = U.paged([n], seed=23)
+    rows, scales = W.row_views(cache)
+    rows[table[0, 1], 0, 64:128] = np.where(np.arange(64) == 6, 0xFE, 0)  # -448, zeros around it
+    scales[table[0, 1], 0, 1] = 254  # times 2^127
+    qb = _queries(1, 23)
+    qb[0, :, 64:128] = 0
+    qb[0, :, 70] = W.to_bf16_bits(np.ones(1, np.float32))
+    d = (U.dev_bf16(qb), U.dev(cache), U.dev(table))
+    out, lse = smla.decode_spans(*d, U.dev(np.array([n], np.int32)), SCALE)
+    want, want_lse = smla.decode_spans(*d, U.dev(np.array([n - 1], np.int32)), SCALE)
+    dims = torch.arange(512, device="cuda") != 70
+    assert torch.isnan(out[0][:, ~dims]).all()
+    # the same two tiles' parts, joined with one of weight 0
+    assert torch.equal(out[0][:, dims], want[0][:, dims]) and torch.equal(lse, want_lse)
+
+
+def test_a_request_whose_scores_are_all_minus_infinity_is_empty():
+    # every token's score is -inf: ln sum exp = -inf, and no weight is left
+    n = 200
+    cache, table = U.paged([n], seed=24)
+    rows, scales = W.row_views(cache)
+    rows[table[0, 0], :n, 64:128] = np.where(np.arange(64) == 6, 0xFE, 0)
+    scales[table[0, 0], :n, 1] = 254
+    qb = _queries(1, 24)
+    qb[0, :, 64:128] = 0
+    qb[0, :, 70] = W.to_bf16_bits(np.ones(1, np.float32))
+    out, lse = smla.decode_spans(U.dev_bf16(qb), U.dev(cache), U.dev(table), U.dev(np.array([n], np.int32)), SCALE)
+    dims = torch.arange(512, device="cuda") != 70
+    assert torch.isneginf(lse).all() and not out[0][:, dims].any()
