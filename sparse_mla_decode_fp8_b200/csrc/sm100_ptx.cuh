@@ -83,6 +83,10 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint64
     }
 }
 
+// Limit of a CTA's waits for its own copies and MMAs in flight before it leaves.  Not the caller's limit, which
+// may be shorter than a copy: what lands after the CTA has left lands in another one's memory.
+constexpr uint64_t kDrainNs = 1000000000ull;
+
 // ---------------------------------------------------------------- fences and barriers
 // Generic-proxy shared-memory writes -> visible to the async proxy (tensor core).
 __device__ __forceinline__ void fence_proxy_async_smem() {

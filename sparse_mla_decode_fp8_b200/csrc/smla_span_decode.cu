@@ -203,12 +203,14 @@ __device__ __forceinline__ void span_code(const Params &p, int b, int len, long 
     count = static_cast<int>(min(static_cast<long long>(kSpan), len - j * kSpan));
 }
 
-// Waits for the scale rows of the tiles published last (the CTA was aborted: nobody else does).
-__device__ __forceinline__ void drain_scales(const Params &p, int k, int lane) {
-    if (lane == 0)
-        for (int i = max(0, k - kRing); i < k; ++i)
-            (void)mbar_wait(sm_bar(kBarRingFull + i % kRing), (i / kRing) & 1, p.timeout_ns);
-    __syncwarp();
+// The tiles whose scale rows may still be on their way when the CTA is aborted, [from, to) in shared memory (the scan's,
+// which is over): registers would be held by every warp of the kernel.
+__device__ __forceinline__ void set_published(int from, int to, int lane) {
+    if (lane == 0) reinterpret_cast<int2 *>(sm_scan())[0] = make_int2(max(0, from), to);
+}
+__device__ __forceinline__ void drain_published() {
+    const int2 tiles = reinterpret_cast<const int2 *>(sm_scan())[0];
+    for (int i = tiles.x; i < tiles.y; ++i) (void)mbar_wait(sm_bar(kBarRingFull + i % kRing), (i / kRing) & 1, kDrainNs);
 }
 
 __device__ __forceinline__ void walk(const Params &p, const Range &r, int lane) {
@@ -234,7 +236,7 @@ __device__ __forceinline__ void walk(const Params &p, const Range &r, int lane) 
             }
             const int m = static_cast<int>(min(32ll, n - base));
             for (int i = 0; i < m; ++i, ++k) {
-                if (!all_wait(kBarRingEmpty + k % kRing, ((k / kRing) & 1) ^ 1, p)) return drain_scales(p, k, lane);
+                if (!all_wait(kBarRingEmpty + k % kRing, ((k / kRing) & 1) ^ 1, p)) return set_published(k - kRing, k, lane);
                 if (lane == i) {
                     Tile t;
                     t.code[0] = code[0];
@@ -266,11 +268,12 @@ __device__ __forceinline__ void walk(const Params &p, const Range &r, int lane) 
             }
         }
     }
-    if (!all_wait(kBarRingEmpty + k % kRing, ((k / kRing) & 1) ^ 1, p)) return drain_scales(p, k, lane);
+    if (!all_wait(kBarRingEmpty + k % kRing, ((k / kRing) & 1) ^ 1, p)) return set_published(k - kRing, k, lane);
     if (lane == 0) {
         sm_ring()[k % kRing].b = -1;
         mbar_arrive(sm_bar(kBarRingFull + k % kRing));
     }
+    set_published(k - kRing + 1, k, lane);  // the end took the place of tile k - kRing, which was read
 }
 
 // ------------------------------------------------------------------ dequantisation
@@ -583,10 +586,10 @@ __device__ __forceinline__ void mma_role(const Params &p, const CUtensorMap *tma
     }
     // every MMA and copy issued must be complete before tensor and shared memory are released
     if (leader) {
-        if (spare_used) (void)mbar_wait(sm_bar(kBarSpare), 0, p.timeout_ns);
-        if (q_pending) (void)mbar_wait(sm_bar(kBarQ), (segments - 1) & 1, p.timeout_ns);
+        if (spare_used) (void)mbar_wait(sm_bar(kBarSpare), 0, kDrainNs);
+        if (q_pending) (void)mbar_wait(sm_bar(kBarQ), (segments - 1) & 1, kDrainNs);
         mma_commit(sm_bar(kBarDrain));
-        (void)mbar_wait(sm_bar(kBarDrain), 0, p.timeout_ns);
+        (void)mbar_wait(sm_bar(kBarDrain), 0, kDrainNs);
     }
     __syncwarp();
 }
@@ -847,7 +850,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             more_registers<kRegsTail>();
             const uint32_t copies = tail_role(p, &tmap_rope, tid & 127, lane);
             if (tid == 32 * (kDequantWarps - 4) && copies)  // the last copy asked for
-                (void)mbar_wait(sm_bar(kBarRope), (copies - 1) & 1, p.timeout_ns);
+                (void)mbar_wait(sm_bar(kBarRope), (copies - 1) & 1, kDrainNs);
             __syncwarp();
         }
     } else if (warp < kMmaWarp) {
@@ -865,6 +868,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after_sync();
         tmem_dealloc(tmem, kTmemCols);
     }
+    // of an aborted CTA, nobody else has waited for the scale rows
+    if (warp == kWalkWarp && lane == 0 && *sm_abort()) drain_published();
     if (tid == 0) p.failed[blockIdx.x] = *sm_abort();
 }
 

@@ -231,9 +231,9 @@ __device__ __forceinline__ void mma_role(const Params &p, const Range &r, const 
     }
     // every MMA and copy issued must be complete before tensor and shared memory are released
     if (leader) {
-        if (loads) (void)mbar_wait(sm_bar(kBarQ), (loads - 1) & 1, p.timeout_ns);
+        if (loads) (void)mbar_wait(sm_bar(kBarQ), (loads - 1) & 1, kDrainNs);
         mma_commit(sm_bar(kBarDrain));
-        (void)mbar_wait(sm_bar(kBarDrain), 0, p.timeout_ns);
+        (void)mbar_wait(sm_bar(kBarDrain), 0, kDrainNs);
     }
     __syncwarp();
 }

@@ -335,3 +335,25 @@ def test_a_request_whose_scores_are_all_minus_infinity_is_empty():
     out, lse = smla.decode_spans(U.dev_bf16(qb), U.dev(cache), U.dev(table), U.dev(np.array([n], np.int32)), SCALE)
     dims = torch.arange(512, device="cuda") != 70
     assert torch.isneginf(lse).all() and not out[0][:, dims].any()
+
+
+@pytest.mark.parametrize("hook", [0, smla.SMLA_DEBUG_SKIP_FIRST_COMMIT])
+@pytest.mark.parametrize("lens", [[100], [1000, 50, 0], [40000, 1, 300], [3000] * 200])
+def test_a_limit_of_a_nanosecond(lens, hook):
+    # shorter than any copy: a request is right or NaN, and the CTAs that gave up have waited for their copies and MMAs
+    cache, table = U.paged(lens, seed=27)
+    args = (U.dev_bf16(_queries(len(lens), 27)), U.dev(cache), U.dev(table), U.dev(np.array(lens, np.int32)), SCALE)
+    want = smla.decode_spans(*args)
+    for i in range(5):
+        ws = _workspace(len(lens))
+        got = smla.decode_spans(*args, workspace=ws, wait_timeout_ns=1, debug_flags=hook)
+        torch.cuda.synchronize()
+        flags = smla.read_error(ws)
+        assert flags in (0, smla.SMLA_FLAG_TIMEOUT) and (flags or not hook)
+        for b, n in enumerate(lens):
+            nan = bool(torch.isnan(got[1][b]).any())
+            assert nan <= (flags != 0) and (nan or not hook or n <= 0)
+            for x, y in zip(got, want):
+                assert torch.isnan(x[b]).all() if nan else torch.equal(x[b], y[b])
+    again = smla.decode_spans(*args)
+    assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])

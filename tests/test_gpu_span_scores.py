@@ -371,3 +371,25 @@ def test_calls_in_a_row_equal_calls_apart():
     for x, y in zip(run(True), run(False)):
         for a, b in zip(x, y):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("hook", [0, smla.SMLA_DEBUG_SKIP_FIRST_COMMIT])
+@pytest.mark.parametrize("lens", [[100], [1000, 50, 0], [40000, 1, 300], [3000] * 200])
+def test_a_limit_of_a_nanosecond(lens, hook):
+    # shorter than any copy: a request is right or NaN, and the CTAs that gave up have waited for their copies and MMAs
+    q, keys, table = _case(lens, 27)
+    args = (U.dev_bf16(q), U.dev_bf16(keys), U.dev(table), U.dev(np.array(lens, np.int32)), SCALE)
+    want = smla.span_scores(*args)
+    for i in range(5):
+        ws = _workspace(*table.shape)
+        got = smla.span_scores(*args, workspace=ws, wait_timeout_ns=1, debug_flags=hook)
+        torch.cuda.synchronize()
+        flags = smla.read_error(ws)
+        assert flags in (0, smla.SMLA_FLAG_TIMEOUT) and (flags or not hook)
+        for b, n in enumerate(lens):
+            spans = -(-n // 64)
+            nan = bool(torch.isnan(got[b]).any())
+            assert nan <= (flags != 0) and (nan or not hook or n <= 0)
+            assert not got[b, spans:].any() and (torch.isnan(got[b, :spans]).all() if nan else torch.equal(got[b], want[b]))
+    again = smla.span_scores(*args)
+    assert torch.equal(again, want)
