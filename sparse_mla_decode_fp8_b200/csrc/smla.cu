@@ -460,10 +460,11 @@ __device__ __forceinline__ void mma_issue_loop(uint32_t tmem, const DecodeParams
             mma_commit(&bars[kBarKvFree + mc]);
         }
     }
-    // every MMA issued must be complete before tensor memory is released
-    if (spare_used) (void)mbar_wait(&bars[kBarSpare], 0, p.timeout_ns);
+    // Q has to have landed and every MMA issued to be complete before shared and tensor memory are released
+    (void)mbar_wait(&bars[kBarQ], 0, kDrainNs);
+    if (spare_used) (void)mbar_wait(&bars[kBarSpare], 0, kDrainNs);
     mma_commit(&bars[kBarDrain]);
-    (void)mbar_wait(&bars[kBarDrain], 0, p.timeout_ns);
+    (void)mbar_wait(&bars[kBarDrain], 0, kDrainNs);
 }
 
 // ------------------------------------------------------------------ worker state
@@ -763,6 +764,8 @@ __device__ __forceinline__ void epilogue_pair(Worker &w, int b, int n, bool ok) 
                      : "memory");
     }
     const bool got = workers_wait<true>(&bars[kBarMl], 0, p, t);
+    // the row comes whatever happens to the peer's waits: not into memory that this CTA has left
+    if (!got && t == kWaiter) (void)mbar_wait(&bars[kBarMl], 0, kDrainNs);
     float *scale = sm_red();
     if (t < kHeads) {
         const float other = got ? sm_peer_lam()[t] : NAN;

@@ -75,3 +75,27 @@ def test_wait_timeout_reports_poisons_and_context_survives(nsplit):
     assert smla.read_error(ws) == 0
     ro, rl = oracle.decode(w.q[0], w.cache, w.block_table, w.topk_idx[0], w.seq_lens, w.sm_scale)
     parity(out, lse, ro, rl)
+
+
+@pytest.mark.parametrize("hook", [0, smla.SMLA_DEBUG_SKIP_FIRST_COMMIT])
+@pytest.mark.parametrize("nsplit", [1, 2, 3])
+def test_a_limit_of_a_nanosecond(nsplit, hook):
+    # shorter than any copy: the CTAs give up at their first wait that does not succeed at once, with Q, MMAs and the
+    # pair's rows on their way, and wait for those before they leave; a request is right or NaN
+    w = W.make_custom(24, 512, [3000] * 24, seed=12)
+    d = device_inputs(w)
+    ws = smla.binding.new_workspace(w.B, w.topk, nsplit=nsplit)
+    args = (d["q"], d["kv_cache"], d["block_table"], d["topk_idx"], d["seq_lens"], d["sm_scale"])
+    want, want_lse = smla.decode(*args, workspace=ws, nsplit=nsplit)
+    for _ in range(5):
+        out, lse = smla.decode(*args, workspace=ws, nsplit=nsplit, wait_timeout_ns=1, debug_flags=hook)
+        torch.cuda.synchronize()
+        flags = smla.read_error(ws)
+        assert flags in (0, smla.SMLA_FLAG_TIMEOUT) and (flags or not hook)
+        for b in range(w.B):
+            if torch.isnan(lse[b]).any():
+                assert flags and torch.isnan(lse[b]).all() and torch.isnan(out[b]).all()
+            else:
+                assert not hook and torch.equal(out[b], want[b]) and torch.equal(lse[b], want_lse[b])
+    again = smla.decode(*args, workspace=ws, nsplit=nsplit)
+    assert torch.equal(again[0], want) and torch.equal(again[1], want_lse) and smla.read_error(ws) == 0
