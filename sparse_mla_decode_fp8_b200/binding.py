@@ -234,6 +234,7 @@ def write_kv(latents, req, pos, block_table, kv_cache, err=None, stream=None) ->
 # ---------------------------------------------------------------- long contexts: spans and reading back
 # These calls take a few microseconds of GPU time at small sizes, so what the binding checks it checks
 # cheaply: one comparison of dtype, device index, shape and density per tensor.
+_INT_MAX = (1 << 31) - 1
 _U8, _I32, _U32, _F32, _BF16 = torch.uint8, torch.int32, torch.uint32, torch.float32, torch.bfloat16
 
 
@@ -268,7 +269,19 @@ def _raw_stream(stream, dev: int) -> int:
 def _size(t, dims: int, name) -> torch.Size:
     if not isinstance(t, torch.Tensor) or t.dim() != dims:
         raise SmlaError(f"{name} must be a tensor of {dims} dimensions")
-    return t.shape
+    shape = t.shape
+    if max(shape) > _INT_MAX:  # ctypes would pass the size modulo 2^32
+        raise SmlaError(f"{name} must have sizes below 2^31, got {list(shape)}")
+    return shape
+
+
+def _options(out_bf16: int, wait_timeout_ns: int, debug_flags: int):
+    """smla_options for a call, or None for the defaults."""
+    if not wait_timeout_ns and not debug_flags:
+        return None
+    if not 0 <= wait_timeout_ns < 1 << 64 or not 0 <= debug_flags < 1 << 32:
+        raise SmlaError("wait_timeout_ns must lie in [0, 2^64) and debug_flags must lie in [0, 2^32)")
+    return ctypes.byref(_Options(0, out_bf16, wait_timeout_ns, debug_flags, 0))
 
 
 @functools.lru_cache(maxsize=None)
@@ -368,15 +381,13 @@ def span_scores(q, keys, block_table, seq_lens, sm_scale, scores=None, workspace
     by its key, summed over the heads.  Without a ``workspace`` one is allocated for the call
     (and its error word is lost)."""
     dev = _current(q, "q")
+    opts = _options(0, wait_timeout_ns, debug_flags)
     B, blocks = _size(block_table, 2, "block_table")
     pages = _size(keys, 3, "keys")[0]
     if scores is None:
         scores = _new(stream, (B, blocks * PAGE_SPANS), _F32, dev)
     if workspace is None:
         workspace = _scratch(span_scores_workspace_bytes(B, blocks), dev, stream)
-    opts = None
-    if wait_timeout_ns or debug_flags:
-        opts = ctypes.byref(_Options(0, 0, wait_timeout_ns, debug_flags, 0))
     rc = library().smla_span_scores(
         _ptr(q, _BF16, dev, (B, HEADS, DIM), "q"), _ptr(keys, _BF16, dev, (pages, PAGE_SPANS, DIM), "keys"),
         _ptr(block_table, _I32, dev, (B, blocks), "block_table"), _ptr(seq_lens, _I32, dev, (B,), "seq_lens"), float(sm_scale),
@@ -394,6 +405,8 @@ def select_spans(scores, seq_lens, nsel: int, keep_first: int = 0, keep_last: in
     B, width = _size(scores, 2, "scores")
     if not 1 <= nsel <= MAX_NSEL:
         raise SmlaError(f"nsel must lie in [1, {MAX_NSEL}]")
+    if keep_first < 0 or keep_last < 0 or keep_first + keep_last > nsel:
+        raise SmlaError("keep_first and keep_last must not be negative and must not add up to more than nsel")
     if spans is None:
         spans = _new(stream, (B, nsel), _I32, dev)
     if topk_idx is None and tokens:
@@ -419,6 +432,7 @@ def decode_spans(q, kv_cache, block_table, seq_lens, sm_scale, spans=None, out=N
     over ``spans`` (int32 [B,nsel]) of them.  Without a ``workspace`` one is allocated for the
     call (and its error word is lost)."""
     dev = _current(q, "q")
+    opts = _options(1, wait_timeout_ns, debug_flags)
     B, blocks = _size(block_table, 2, "block_table")
     pages = _size(kv_cache, 2, "kv_cache")[0]
     nsel, listed = 0, None
@@ -433,9 +447,6 @@ def decode_spans(q, kv_cache, block_table, seq_lens, sm_scale, spans=None, out=N
         lse = _new(stream, (B, HEADS), _F32, dev)
     if workspace is None:
         workspace = _scratch(decode_spans_workspace_bytes(B), dev, stream)
-    opts = None
-    if wait_timeout_ns or debug_flags:
-        opts = ctypes.byref(_Options(0, 1, wait_timeout_ns, debug_flags, 0))
     rc = library().smla_decode_spans(
         _ptr(q, _BF16, dev, (B, HEADS, DIM), "q"), _ptr(kv_cache, _U8, dev, (pages, PAGE_BYTES), "kv_cache"),
         _ptr(block_table, _I32, dev, (B, blocks), "block_table"), listed, nsel, _ptr(seq_lens, _I32, dev, (B,), "seq_lens"),

@@ -91,3 +91,24 @@ def test_entry_points_take_their_argument_counts(lib):
         assert len(fn.argtypes) == len(args)
         with pytest.raises((TypeError, ctypes.ArgumentError)):
             fn(*args[:-1])
+
+
+def test_binding_refuses_numbers_beyond_the_abi_types(monkeypatch):
+    # ctypes would take them modulo 2^32 (2^64) and run with another number
+    monkeypatch.setattr(smla.binding, "_current", lambda t, name: 0)
+
+    def meta(*shape, dtype=torch.int32):
+        return torch.empty(shape, dtype=dtype, device="meta")
+
+    wide = 2**32 + 5
+    cache, keys, one = meta(1, 149504, dtype=torch.uint8), meta(1, 4, 512, dtype=torch.bfloat16), meta(1, 1)
+    q, f32 = meta(1, 64, 512, dtype=torch.bfloat16), torch.float32
+    calls = [lambda: smla.select_spans(meta(1, wide, dtype=f32), meta(1), 2), lambda: smla.select_spans(meta(wide, 1, dtype=f32), meta(wide), 2),
+             lambda: smla.span_keys(cache, one, meta(1), meta(wide), meta(wide), keys), lambda: smla.read_kv(cache, meta(wide), meta(wide), one)]
+    for first, last in ((2**32, 0), (0, 2**32), (2**32 + 1, 1), (-(2**32), 0), (-1, 0), (1, 2), (3, 0)):
+        calls.append(lambda first=first, last=last: smla.select_spans(meta(1, 8, dtype=f32), meta(1), 2, keep_first=first, keep_last=last))
+    for kw in (dict(wait_timeout_ns=-1), dict(wait_timeout_ns=2**64), dict(debug_flags=2**32), dict(debug_flags=-1)):
+        calls += [lambda kw=kw: smla.decode_spans(q, cache, one, meta(1), 0.1, **kw), lambda kw=kw: smla.span_scores(q, keys, one, meta(1), 0.1, **kw)]
+    for i, call in enumerate(calls):
+        with pytest.raises(smla.SmlaError, match="must"):
+            call()
