@@ -357,3 +357,199 @@ def test_a_limit_of_a_nanosecond(lens, hook):
                 assert torch.isnan(x[b]).all() if nan else torch.equal(x[b], y[b])
     again = smla.decode_spans(*args)
     assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
+
+
+# ---------------------------------------------------------------- many tiles in a CTA
+def _tiles_per_cta(tiles):
+    return -(-tiles // torch.cuda.get_device_properties(0).multi_processor_count)
+
+
+def test_a_segment_moves_its_reference_three_times():
+    # 300 requests share one sequence of four tiles whose scores lie 70 log2 units above each other, so that each
+    # tile of a segment raises the reference and rescales what was summed.  Dims group g is nonzero in tile g only, and so
+    # large there that its share, 2^-70 a raise, stays a normal number: every factor shows in the output's own digits.
+    B, n = 300, 512
+    assert _tiles_per_cta(B * 4) >= 8  # whole requests inside a CTA
+    rng = np.random.default_rng(20)
+    cache = np.full((2, W.PAGE_BYTES), 0xFF, np.uint8)
+    lat = np.zeros((n, 512), np.float32)
+    tile = np.arange(n) // 128
+    for g in range(4):
+        lat[tile == g, 64 * g:64 * g + 64] = rng.standard_normal((128, 64)) * 2.0 ** (100 - 70 * g)
+    # scores: 8 rope dims that add up to the tile's height and up to two more
+    lat[:, 448:456] = (70 * tile + rng.random(n) * 2).astype(np.float32)[:, None] / 8
+    W.write_tokens(cache, np.arange(n) // 256, np.arange(n) % 256, lat)
+    table = np.tile(np.array([[1, 0]], np.int32), (B, 1))
+    cache = cache[::-1].copy()  # page 1 holds the first half
+    qv = np.zeros((B, 64, 512), np.float32)
+    qv[:, :, 448:456] = 1.0
+    qv[:, 1::2, 448:456] = -1.0  # falling scores: the reference of the odd heads stays
+    scale = float(np.log(2.0))
+    ws = _workspace(B)
+    out, lse = smla.decode_spans(U.dev_bf16(W.to_bf16_bits(qv)), U.dev(cache), U.dev(table), U.dev(np.full(B, n, np.int32)), scale,
+                                 workspace=ws)
+    assert smla.read_error(ws) == 0
+    out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    o, l, mean_abs, size = U.attention(qv[0].astype(np.float64), cache, table, 0, np.arange(n), scale)
+    # 8 exact products are added (the zeros add nothing), then one product and one sum in fp32, and the references'
+    # roundings, each 2^-23 of the largest score at most; exp2 of both 2^-21
+    e = 16 * 2.0 ** -23 * size + 2.0 ** -20
+    # a request cut between two CTAs: its parts are joined by fp32 weights 2^(lambda_i - max), so that tokens whose weight
+    # relative to the largest lies below the least normal number, 2^-126, may count for nothing
+    k = U.latents(cache, table, 0, np.arange(n))
+    s = scale * (qv[0].astype(np.float64) @ k.T)
+    p = np.exp(s - s.max(axis=1, keepdims=True))
+    lost = np.minimum(p, 2.0 ** -126) @ np.abs(k)
+    per = _tiles_per_cta(B * 4)
+    for b in range(B):
+        off = np.abs(out[b] - o)
+        # an odd head's groups behind the first fall below the normal numbers: 2^-120 covers those
+        bound = mean_abs * (2.0 ** -8 * (1 + 2 * e) + 2 * e + (n + 16) * 2.0 ** -23) + 2.0 ** -8 * (np.abs(o) + off) + 2.0 ** -120
+        if 4 * b // per != (4 * b + 3) // per:
+            bound = bound + lost
+        assert (off <= bound).all(), (b, float((off / bound).max()))
+        assert (np.abs(lse[b] - l) <= e + (n + 16) * 2.0 ** -24 + 2.0 ** -21 * (1 + np.abs(l))).all(), b
+
+
+@pytest.mark.parametrize("listed", [False, True])
+def test_segments_of_more_than_32_tiles(listed):
+    # one request of 40 tiles for every SM and a part of one, over the same 8 pages again and again (or, listed, 1,024
+    # requests' worth of spans over them): the walk looks pages up 32 tiles at a time
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    pages = 8
+    if listed:
+        B, nsel = 40 * sms // 512 + 1, 1024
+        lens = [256 * pages] * B
+        cache, one = U.paged([256 * pages], seed=21)
+        table = np.tile(one, (B, 1))
+        spans = np.random.default_rng(21).integers(0, 4 * pages, (B, nsel)).astype(np.int32)
+        tiles = B * nsel // 2
+        counts = [np.repeat(np.bincount(s, minlength=4 * pages), 64) for s in spans]
+    else:
+        B, n = 1, 40 * 128 * sms + 77
+        cache, one = U.paged([256 * pages], seed=21)
+        table = np.tile(one, (1, -(-n // (256 * pages))))[:, :-(-n // 256)]
+        lens, spans, tiles = [n], None, -(-n // 128)
+        counts = [np.bincount(np.arange(n) % (256 * pages), minlength=256 * pages)]
+    assert _tiles_per_cta(tiles) > 32
+    qb = _queries(B, 21)
+    ws = _workspace(B)
+    out, lse = smla.decode_spans(U.dev_bf16(qb), U.dev(cache), U.dev(np.ascontiguousarray(table)), U.dev(np.array(lens, np.int32)), SCALE,
+                                 spans=None if spans is None else U.dev(spans), workspace=ws)
+    assert smla.read_error(ws) == 0
+    out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    k = U.latents(cache, table, 0, np.arange(256 * pages))
+    q = independent.q_values(qb)
+    size = max(SCALE * float((np.abs(q[b]) @ np.abs(k).T).max()) for b in range(B))
+    e = 512 * 2.0 ** -23 * size + 2.0 ** -21
+    adds = _tiles_per_cta(tiles) * 128 + sms + 16  # a CTA's own tokens, then the parts
+    for b in range(B):
+        s = SCALE * (q[b] @ k.T)
+        p = counts[b] * np.exp(s - s.max(axis=1, keepdims=True))
+        total = p.sum(axis=1, keepdims=True)
+        o, l, mean_abs = p @ k / total, (s.max(axis=1, keepdims=True) + np.log(total))[:, 0], p @ np.abs(k) / total
+        off = np.abs(out[b] - o)
+        bound = mean_abs * (2.0 ** -8 * (1 + 2 * e) + 2 * e + adds * 2.0 ** -23) + 2.0 ** -8 * (np.abs(o) + off)
+        assert (off <= bound).all(), (b, float((off / bound).max()))
+        assert (np.abs(lse[b] - l) <= e + adds * 2.0 ** -24 + 2.0 ** -21 * (1 + np.abs(l))).all(), b
+
+
+@pytest.mark.parametrize("lens", [[40000], [9000, 300, 17000, 1]])
+def test_long_sequences_in_the_norm(lens):
+    # Beside the element-wise bound: weights and outputs are each off by a rounding of rms 2^-8 / sqrt(3) at most,
+    # independent from token to token; over latents of mean zero both are that share of the norm, together
+    # 2^-8 sqrt(2 / 3) = 3.2e-3, below 4e-3
+    out, _ = _run(lens, seed=22)
+    cache, table = U.paged(lens, 22)
+    q = independent.q_values(_queries(len(lens), 22))
+    got = out.double().cpu().numpy()
+    for b, n in enumerate(lens):
+        want = U.attention(q[b], cache, table, b, np.arange(n), SCALE)[0]
+        assert np.linalg.norm(got[b] - want) <= 4e-3 * np.linalg.norm(want), b
+
+
+def test_captured_behind_two_streams_and_without_a_workspace():
+    # a capture where the call's kernels follow work of two streams, and one where the workspace is allocated inside
+    lens = np.array([3000, 700], np.int32)
+    cache, table = U.paged(lens, seed=25)
+    q, c, t, sl = U.dev_bf16(_queries(2, 25)), U.dev(cache), U.dev(table), U.dev(lens)
+    keys = torch.zeros((len(cache), 4, 512), dtype=torch.bfloat16, device="cuda")
+    keys.normal_(generator=torch.Generator("cuda").manual_seed(5))
+    want = smla.decode_spans(q, c, t, sl, SCALE)
+    want_scores = smla.span_scores(q, keys, t, sl, SCALE)
+    ws, ws2 = _workspace(2), torch.zeros(smla.span_scores_workspace_bytes(*t.shape), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for given in (True, False):
+        a, b = torch.zeros_like(q), torch.zeros_like(sl)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            main, side = torch.cuda.current_stream(), torch.cuda.Stream()
+            side.wait_stream(main)
+            a.copy_(q)
+            with torch.cuda.stream(side):
+                b.copy_(sl)
+                b.mul_(1)
+            main.wait_stream(side)
+            out, lse = smla.decode_spans(a, c, t, b, SCALE, workspace=ws if given else None)
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                b.add_(0)
+            a.mul_(1)
+            main.wait_stream(side)
+            scores = smla.span_scores(a, keys, t, b, SCALE, workspace=ws2 if given else None)
+        for _ in range(3):
+            for x in (a, b, out, lse, scores):
+                x.zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want[0]) and torch.equal(lse, want[1]) and torch.equal(scores, want_scores)
+
+
+def test_more_requests_than_threads_of_a_cta():
+    # the lengths of two or three requests a thread, summed by every CTA and written out for the join
+    rng = np.random.default_rng(28)
+    lens = list(rng.integers(-1, 140, 2000))
+    lens[0], lens[897], lens[1999] = 0, 1500, 129
+    _run(lens, seed=28)
+
+
+def test_pages_behind_4_gib():
+    # a pool of 5.3 GB, the requests in its last pages; spans read, scored and attended there
+    lens = [1000, 513]
+    cache, table = U.paged(lens, seed=29)
+    pages, first = 35500, 35500 - len(cache)
+    assert first * W.PAGE_BYTES > 1 << 32
+    pool = torch.empty((pages, W.PAGE_BYTES), dtype=torch.uint8, device="cuda")
+    pool[first:] = U.dev(cache)
+    far = np.where(table >= 0, table + first, -1).astype(np.int32)
+    qb = _queries(2, 29)
+    sl, ws = U.dev(np.array(lens, np.int32)), _workspace(2)
+    out, lse = smla.decode_spans(U.dev_bf16(qb), pool, U.dev(far), sl, SCALE, workspace=ws)
+    assert smla.read_error(ws) == 0
+    U.check_decode(out, lse, independent.q_values(qb), cache, table, [np.arange(n) for n in lens], SCALE)
+    req = np.repeat(np.arange(2), lens).astype(np.int32)
+    pos = np.concatenate([np.arange(n) for n in lens]).astype(np.int32)
+    for p, t in ((pool, far), (U.dev(cache), table)):
+        rows = smla.read_kv(p, U.dev(req), U.dev(pos), U.dev(t), out_dtype=torch.float32)
+        keys = torch.zeros((p.shape[0], 4, 512), dtype=torch.bfloat16, device="cuda")
+        spans = [np.arange(-(-n // 64)) for n in lens]
+        smla.span_keys(p, U.dev(t), sl, U.dev(np.repeat(np.arange(2), [len(s) for s in spans]).astype(np.int32)),
+                       U.dev(np.concatenate(spans).astype(np.int32)), keys)
+        got = (rows, keys[-len(cache):].clone(), smla.span_scores(U.dev_bf16(qb), keys, U.dev(t), sl, SCALE))
+        if p is pool:
+            want = got
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and not torch.isnan(got[0]).any() and got[1].any()
+
+
+def test_keys_behind_4_gib():
+    # 1.1 million pages of keys (4.5 GB): a request's last ones score as those of a small pool
+    lens, pages = [9000, 300], 1_100_000
+    rng = np.random.default_rng(30)
+    table = rng.permutation(40)[:36 * 1].astype(np.int32)
+    table = np.stack([table, np.r_[np.setdiff1d(np.arange(40), table)[:2], np.full(34, -1)]]).astype(np.int32)
+    small = torch.randn((40, 4, 512), device="cuda", generator=torch.Generator("cuda").manual_seed(30)).to(torch.bfloat16)
+    pool = torch.empty((pages, 4, 512), dtype=torch.bfloat16, device="cuda")
+    pool[-40:] = small
+    far = np.where(table >= 0, table + pages - 40, -1).astype(np.int32)
+    q, sl = U.dev_bf16(_queries(2, 30)), U.dev(np.array(lens, np.int32))
+    assert torch.equal(smla.span_scores(q, pool, U.dev(far), sl, SCALE), smla.span_scores(q, small, U.dev(table), sl, SCALE))

@@ -212,3 +212,34 @@ def test_select_spans_on_another_stream_and_in_a_graph():
     torch.cuda.synchronize()
     want = U.select(y, lens, 5, 1, 1)
     assert np.array_equal(spans.cpu().numpy(), want[0]) and np.array_equal(idx.cpu().numpy(), want[1])
+
+
+def test_span_keys_of_lists_longer_than_the_grid():
+    # about five spans a block: full, partial and skipped ones in any order, some listed again
+    lens = np.array([5000, 63, 1, 4097, 640, 2222, 0, 130], np.int32)
+    cache, table = U.paged(lens, seed=26)
+    table[4, 1] = -1
+    n = 5 * 4 * torch.cuda.get_device_properties(0).multi_processor_count + 37
+    rng = np.random.default_rng(26)
+    req = rng.integers(-1, len(lens) + 1, n).astype(np.int32)
+    have = np.array([-(-max(int(x), 0) // 64) for x in lens])
+    span = np.where(rng.random(n) < 0.2, rng.integers(-3, 200, n), (rng.random(n) * have[req % len(lens)]).astype(np.int64)).astype(np.int32)
+    last = rng.random(n) < 0.2  # the partial ones more often
+    span[last] = (have[req % len(lens)] - 1)[last]
+    keys = torch.full((len(cache), 4, 512), 3.0, dtype=torch.bfloat16, device="cuda")
+    err = _err()
+    smla.span_keys(U.dev(cache), U.dev(table), U.dev(lens), U.dev(req), U.dev(span), keys, err=err)
+    assert int(err.item()) == smla.SMLA_FLAG_BAD_PAGE
+    got = keys.double().cpu().numpy()
+    touched = np.zeros(got.shape[:2], bool)
+    live = 0
+    for b, j in set(zip(req.tolist(), span.tolist())):
+        if not (0 <= b < len(lens) and 0 <= j < have[b]) or table[b, j // 4] < 0:
+            continue
+        live += 1
+        want = U.span_mean(cache, table, lens, b, j)
+        mean_abs = np.abs(U.latents(cache, table, b, np.arange(64 * j, min(64 * j + 64, lens[b])))).mean(axis=0)
+        bound = 2.0 ** -8 * np.abs(want) + 18 * 2.0 ** -24 * mean_abs  # as for single spans
+        assert (np.abs(got[table[b, j // 4], j % 4] - want) <= bound).all(), (b, j)
+        touched[table[b, j // 4], j % 4] = True
+    assert live > 150 and (got[~touched] == 3.0).all()
