@@ -44,7 +44,7 @@ constexpr int kSmemQ = 0;                      // 64 KB: 8 K-blocks x [64 heads 
 constexpr int kSmemKeys = kSmemQ + 65536;      // 128 KB: 8 K-blocks x [128 spans x 128 B]
 constexpr int kSmemCodes = kSmemKeys + 131072; // [128] key rows of the tile being loaded
 constexpr int kSmemRed = kSmemCodes + 512;     // [4][64] per-warp maxima or sums
-constexpr int kSmemMax = kSmemRed + 1024;      // [64]
+constexpr int kSmemMax = kSmemRed + 1024;      // [64] maxima of the tile, 0 where it has none
 constexpr int kSmemScan = kSmemMax + 256;
 constexpr int kSmemBars = kSmemScan + 8 * (kThreads / 32 + 2) + 8;
 enum Bar : int {
@@ -241,7 +241,7 @@ __device__ __forceinline__ void mma_role(const Params &p, const Range &r, const 
 // ------------------------------------------------------------------ x, maxima, sums
 // Warp q (0..3) owns tensor-memory lanes 32q..: a span a thread, 64 heads.
 __device__ __forceinline__ void stat_role(const Params &p, const Range &r, uint32_t tmem, int q, int lane) {
-    float *red = reinterpret_cast<float *>(g_smem + kSmemRed), *top = reinterpret_cast<float *>(g_smem + kSmemMax);
+    float *red = reinterpret_cast<float *>(g_smem + kSmemRed), *base = reinterpret_cast<float *>(g_smem + kSmemMax);
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * q) << 16);
     const int t = 32 * q + lane;
     uint32_t n = 0;
@@ -276,7 +276,12 @@ __device__ __forceinline__ void stat_role(const Params &p, const Range &r, uint3
             red[q * 64 + 32 * half + lane] = warp_transpose_reduce<true, 32>(y, lane);
         }
         named_barrier_sync(kBarIdStat, kStatThreads);
-        if (t < kHeads) top[t] = fmaxf(fmaxf(red[t], red[64 + t]), fmaxf(red[128 + t], red[192 + t]));
+        float top = 0.0f;  // of head t
+        if (t < kHeads) {
+            top = fmaxf(fmaxf(red[t], red[64 + t]), fmaxf(red[128 + t], red[192 + t]));
+            // the maximum passes NaN over: where it is -inf, weights 2^(x - 0) are 0 for -inf and NaN for NaN
+            base[t] = top == -INFINITY ? 0.0f : top;
+        }
         named_barrier_sync(kBarIdStat, kStatThreads);
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
@@ -285,9 +290,7 @@ __device__ __forceinline__ void stat_role(const Params &p, const Range &r, uint3
             tmem_wait_ld();
 #pragma unroll
             for (int h = 0; h < 32; ++h) {
-                const float s = valid ? x[h] * p.scale_log2 : -INFINITY;
-                // the test is on the score: the maximum (which passes NaN over) may be -inf beside a NaN
-                x[h] = s == -INFINITY ? 0.0f : fast_exp2(s - top[32 * half + h]);
+                x[h] = valid ? fast_exp2(x[h] * p.scale_log2 - base[32 * half + h]) : 0.0f;
             }
             red[q * 64 + 32 * half + lane] = warp_transpose_reduce<false, 32>(x, lane);
         }
@@ -295,7 +298,7 @@ __device__ __forceinline__ void stat_role(const Params &p, const Range &r, uint3
         __syncwarp();
         if (lane == 0) mbar_arrive(sm_bar(kBarSFree + buf));
         named_barrier_sync(kBarIdStat, kStatThreads);
-        if (t < kHeads) stats[t] = make_float2(top[t], (red[t] + red[64 + t]) + (red[128 + t] + red[192 + t]));
+        if (t < kHeads) stats[t] = make_float2(top, (red[t] + red[64 + t]) + (red[128 + t] + red[192 + t]));
     }
 }
 
