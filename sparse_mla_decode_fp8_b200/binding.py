@@ -267,11 +267,12 @@ def _raw_stream(stream, dev: int) -> int:
 
 
 def _size(t, dims: int, name) -> torch.Size:
-    if not isinstance(t, torch.Tensor) or t.dim() != dims:
+    if not isinstance(t, torch.Tensor):
         raise SmlaError(f"{name} must be a tensor of {dims} dimensions")
     shape = t.shape
-    if max(shape) > _INT_MAX:  # ctypes would pass the size modulo 2^32
-        raise SmlaError(f"{name} must have sizes below 2^31, got {list(shape)}")
+    # ctypes would pass a size modulo 2^32 (sizes between the first and the last are fixed ones, which _ptr checks)
+    if len(shape) != dims or shape[0] > _INT_MAX or shape[-1] > _INT_MAX:
+        raise SmlaError(f"{name} must be a tensor of {dims} dimensions below 2^31, got {list(shape)}")
     return shape
 
 
