@@ -506,9 +506,9 @@ def test_captured_behind_two_streams_and_without_a_workspace():
 
 
 def test_more_requests_than_threads_of_a_cta():
-    # the lengths of two or three requests a thread, summed by every CTA and written out for the join
+    # the lengths of two or three requests a thread, nine of ten of them empty, summed by every CTA and written out for the join
     rng = np.random.default_rng(28)
-    lens = list(rng.integers(-1, 140, 2000))
+    lens = list(np.where(rng.random(2000) < 0.1, rng.integers(1, 140, 2000), rng.integers(-1, 1, 2000)))
     lens[0], lens[897], lens[1999] = 0, 1500, 129
     _run(lens, seed=28)
 
