@@ -84,7 +84,8 @@ extern "C" {
 typedef struct smla_options {
     int nsplit;                  /* topk splits per request; 0 = built-in heuristic */
     int out_bf16;                /* 0: out is fp32; 1: out is bf16 (see smla_decode_ex) */
-    uint64_t wait_timeout_ns;    /* bound on every in-kernel wait; 0 = 1 s */
+    uint64_t wait_timeout_ns;    /* bound on every in-kernel wait; 0 = 1 s.  A CTA that gave up still waits
+                                  * for its own copies and MMAs in flight, for at most 1 s each */
     uint32_t debug_flags;        /* test hooks, 0 in normal use (see SMLA_DEBUG_*) */
     uint32_t reserved1;
 } smla_options;
@@ -277,19 +278,22 @@ int smla_span_keys(const uint8_t *kv_cache, const int32_t *block_table, const in
  * smla_span_scores -- how much of a query's attention each span of its request should get,
  * estimated from the span keys: score[b][j] = sum over the 64 heads of
  * softmax_j(sm_scale <q[b][h], key_j>), the softmax over the request's spans; the scores of a
- * request add up to 64.
+ * request add up to 64.  A span counts the same however many tokens it has: a last span of
+ * one token is scored like one of 64 (smla_select_spans keeps it with keep_last >= 1).
  *   q           device, bf16 [B][H][512], as for the decode that follows
  *   keys        device, bf16 [num_pages][4][512], as smla_span_keys writes them
  *   scores      device, fp32 [B][4 max_blocks] (written): 0 behind the request's last span; a
  *               span in a page outside [0, num_pages) takes no part, scores 0 and sets
- *               SMLA_FLAG_BAD_PAGE
+ *               SMLA_FLAG_BAD_PAGE; a NaN in the query or in a key makes the other spans of
+ *               the request NaN
  *   workspace   device scratch of at least smla_span_scores_workspace_bytes(B, max_blocks)
  *               bytes, 256-byte aligned, its first 4 bytes the sticky error word (see
  *               smla_decode); not shared by calls that may run at the same time
  *   opts        NULL, or options with nsplit 0 and out_bf16 0 (wait_timeout_ns, debug_flags); a
  *               wait that ran out makes the scores of the requests it touched NaN
- *   H must be 64; 1 <= max_blocks <= SMLA_MAX_SPANS / 4.  Two launches on `stream`; sums in a
- *   fixed order (reproducible bit for bit).
+ *   H must be 64; 1 <= B <= 65535; 1 <= max_blocks <= SMLA_MAX_SPANS / 4.  Two launches on
+ *   `stream`; sums in a fixed order (reproducible bit for bit).  A part of the work grows with
+ *   the square of a request's spans; above 16,384 (a million tokens) it is the larger part.
  */
 int smla_span_scores(const void *q, const void *keys, const int32_t *block_table, const int32_t *seq_lens,
                      float sm_scale, float *scores, int B, int H, int max_blocks, int num_pages, void *workspace,
@@ -322,7 +326,9 @@ int smla_select_spans(const float *scores, int width, const int32_t *seq_lens, i
  *               spans (-1 among them) hold no token; an entry listed twice counts twice;
  *               1 <= nsel <= SMLA_MAX_NSEL
  *   out         device, bf16 [B][H][512], 16-byte aligned (written): softmax weights enter the
- *               second product as bf16, the sums are fp32, the result is rounded once
+ *               second product as one bf16 term (smla_decode: two), the sums are fp32, the
+ *               result is rounded once: over random latents 1.6e-3 of the norm from 64 bits,
+ *               1.1e-3 of it the bf16 output
  *   lse         device, fp32 [B][H] (written)
  *   workspace   device scratch of at least smla_decode_spans_workspace_bytes(B) bytes, 256-byte
  *               aligned, its first 4 bytes the sticky error word (see smla_decode).  Nothing
@@ -330,8 +336,8 @@ int smla_select_spans(const float *scores, int width, const int32_t *seq_lens, i
  *               captured graphs among them, must not share one.
  *   kv_cache    32-byte aligned here
  *   opts        NULL, or options with nsplit 0 and out_bf16 1 (wait_timeout_ns, debug_flags)
- *   The other arguments are those of smla_decode.  A sequence longer than 256 max_blocks is
- *   cut there.  A request without tokens gets out = 0, lse = -inf; a token whose score is -inf
+ *   The other arguments are those of smla_decode, with 1 <= B <= 65535.  A sequence longer
+ *   than 256 max_blocks is cut there.  A request without tokens gets out = 0, lse = -inf; a token whose score is -inf
  *   weighs 0, a head that has no other gets lse = -inf; tokens in a page outside
  *   [0, num_pages) count for nothing and set SMLA_FLAG_BAD_PAGE.  A wait that ran out makes the
  *   rows of the requests it touched NaN and sets SMLA_FLAG_TIMEOUT.

@@ -22,9 +22,10 @@
 // softmax and the epilogue; of the last, one warp issues the MMAs and one walks the CTA's range and
 // publishes a tile's pages in a ring.
 //
-// What bounds it (64 requests of 65536 tokens, 860 us: 2.85 TB/s, 640 TFLOP/s; a tile takes about 7,100
-// cycles): the chain of one tile.  Q, one converted tile and P^T fill shared memory, so a chunk is
-// stored when the second product of the tile before has released it.  By clock stamps, from the hand-over
+// What bounds it (64 requests of 65536 tokens, 860 to 917 us from one GPU to the other at the 1 kW cap: 2.68 to
+// 2.86 TB/s, 600 to 640 TFLOP/s; a tile takes about 7,100 cycles): the chain of one tile.  Q, one converted
+// tile and P^T fill shared memory, so a chunk is stored when the second product of the tile before has
+// released it.  By clock stamps, from the hand-over
 // of P^T: second product 1,950 cycles, the last chunk stored 1,000 later (the first pair's MMAs run by
 // then), scores complete 2,000 after that, weights handed over 1,700 after that.  Under the chain lies shared
 // memory's port: the MMAs read 128 bytes a cycle for 3,100 cycles, the conversions store for 1,000, and the
@@ -33,7 +34,10 @@
 // the place of P^T 16 %, row loads held back until P^T is done 14 %; the last nope group by TMA through
 // 8 KB of its own gains nothing, rope values by TMA straight into the tile 3 %.  With few tokens a start
 // of 15,000 cycles counts: cold instructions, the lookups, one tile's chain of loads and barriers; and a
-// part's 128 KB, stored in 5,000 cycles and read again by the join.
+// part's 128 KB, stored in 5,000 cycles and read again by the join.  The join has a warp per (request, head), which walks
+// the request's parts in turn: with one long request that is 64 warps on 8 SMs for up to 148 parts, and most of the
+// call (one request of 32,768 tokens 66 us, of 131,072 95 us).  With a list every two entries are a tile, -1 or not: 64
+// requests of 300 tokens with 64 entries take 73 us.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

@@ -4,17 +4,21 @@
 // Mathematics.  x_hj = sm_scale log2(e) q_h . key_j (exact bf16 products, fp32 sums).  The first kernel
 // leaves x and, per 128 spans and head, their maximum m and sum l = sum_j 2^(x - m); the second
 // joins these to lambda_h = M + log2 sum l 2^(m - M) and sums 2^(x_hj - lambda_h) over the heads in a
-// fixed order.  All of it is fp32.  The second is launched while the first still runs and waits for it
-// (2 us a call less); it reads what the first wrote through L2.
+// fixed order.  All of it is fp32.  The second is launched while the first still runs and waits for it, before it
+// reads anything (2 us a call less); it reads what the first wrote through L2.
 //
 // Work: 1,024 bytes and 65,536 flops per span, 64 flop/byte: bound by the keys' way through HBM.  One CTA
 // per SM walks an equal contiguous part of all requests' 128-span tiles (lengths are read on the
 // device) and keeps up to 7 of the 8 key chunks [128 spans x 64 dims] in flight; Q stays in
 // shared memory for the CTA's tiles of a request.  x (256 bytes a span) goes through L2.
-// 64 requests of 65,536 tokens take 28.3 us in a graph for a floor of 11 (67 MB of keys): besides HBM the
-// load-store pipe counts, a cycle for 32 bytes of keys and of x (x by 16-byte stores, half a sector
-// each: 30.8 us), and the chain start - load - MMA - statistics - second kernel, which is nearly all of the
-// 10 to 12.6 us that few spans take.
+// 64 requests of 65,536 tokens take 26.5 us in a graph for a floor of 11 (67 MB of keys, which are partly in L2
+// from one call to the next; 39 us with L2 flushed, launch included): besides HBM the load-store pipe counts, a
+// cycle for 32 bytes of keys and of x (x by 16-byte stores, half a sector each: 2 us more), and the chain start -
+// load - MMA - statistics - second kernel, which is nearly all of the 10 to 12 us that few spans take.  The ranges are
+// whole tiles: those 512 tiles are 4 for each of 128 CTAs, and 20 SMs get none.
+// Every block of the second kernel reads the statistics of all tiles of its request, n^2 / 16 bytes for n spans in
+// all: as much as the keys at 16,384 spans (a million tokens; one such request takes 22 us, eight 62 us), and
+// more than all else beyond.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

@@ -27,9 +27,11 @@ static_assert(kSpan == 64 && kPageTokens % kSpan == 0, "a span is a quarter of a
 // nope chunks, thread (g, c) of 8 x 28 chunk c of the rows g, g + 8, ..; two warps the rope chunks, thread
 // (g, c) of 8 x 8.  The 8 partial sums of a dim are added in shared memory.  The lookups of a span
 // (request and span, length and page) are made ahead.
-// 584 bytes are read per token and 1,024 written per span: 438.5 MB for 12,174 spans take 96 us, 70 % of
-// the measured copy bandwidth.  Instructions to issue bound it next to HBM: 144 us when warps mixed
-// nope and rope chunks, 133 us with rows by loads (whose pipe takes a cycle for 32 bytes).
+// 584 bytes are read per token and 1,024 written per span: 438.5 MB for 11,426 spans take 93 to 95 us, 71 % of
+// the measured copy bandwidth.  Instructions to issue bound it next to HBM (ncu: issue slots 70 % busy, DRAM 57 % of its
+// peak, the load-store pipe 44 %): 144 us when warps mixed nope and rope chunks, 133 us with rows by loads (whose pipe
+// takes a cycle for 32 bytes).  A block has one stage, so nothing of it is in flight while it sums; the other three
+// blocks of the SM cover that in part.
 constexpr int kKeyGroups = 8;
 constexpr int kKeyNopeThreads = kKeyGroups * kNopeChunks;  // 224
 constexpr int kKeyRopeChunks = kRowChunks - kNopeChunks;
