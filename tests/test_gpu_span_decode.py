@@ -553,3 +553,37 @@ def test_keys_behind_4_gib():
     far = np.where(table >= 0, table + pages - 40, -1).astype(np.int32)
     q, sl = U.dev_bf16(_queries(2, 30)), U.dev(np.array(lens, np.int32))
     assert torch.equal(smla.span_scores(q, pool, U.dev(far), sl, SCALE), smla.span_scores(q, small, U.dev(table), sl, SCALE))
+
+
+def test_two_graphs_at_once_and_stream_handles():
+    # graphs with a workspace each, replayed on two streams at the same time; streams given as plain handles
+    lens = [[3000, 500, 41], [20000]]
+    args, want, keys, want_scores = [], [], [], []
+    for i, n in enumerate(lens):
+        cache, table = U.paged(n, seed=31 + i)
+        args.append((U.dev_bf16(_queries(len(n), 31 + i)), U.dev(cache), U.dev(table), U.dev(np.array(n, np.int32)), SCALE))
+        keys.append(torch.randn((len(cache), 4, 512), device="cuda", generator=torch.Generator("cuda").manual_seed(i)).to(torch.bfloat16))
+        want.append(smla.decode_spans(*args[i]))
+        want_scores.append(smla.span_scores(args[i][0], keys[i], *args[i][2:]))
+    torch.cuda.synchronize()
+    graphs, got, spaces, streams = [], [], [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for i in range(2):
+        spaces.append((_workspace(len(lens[i])), torch.zeros(smla.span_scores_workspace_bytes(*args[i][2].shape), dtype=torch.uint8, device="cuda")))
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            scores = smla.span_scores(args[i][0], keys[i], *args[i][2:], workspace=spaces[i][1])
+            got.append((*smla.decode_spans(*args[i], workspace=spaces[i][0]), scores))
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for i in range(2):
+        for a, b in zip(got[i], (*want[i], want_scores[i])):
+            assert torch.equal(a, b)
+    for handle in (0, streams[0].cuda_stream):
+        out = smla.decode_spans(*args[0], stream=handle)
+        torch.cuda.synchronize()
+        assert torch.equal(out[0], want[0][0]) and torch.equal(out[1], want[0][1])
